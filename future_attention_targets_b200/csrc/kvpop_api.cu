@@ -17,6 +17,7 @@
 
 #include "kvpop.h"
 #include "kvpop_cache.h"
+#include "kvpop_host.h"
 
 namespace kvpop {
 cudaError_t launch_row_lse(const AttnParams& p, int head_dim, int sm_count, cudaStream_t stream);
@@ -363,6 +364,18 @@ struct EventSet {
 };
 
 }  // namespace
+
+namespace kvpop {
+kvpop_status host_fail(kvpop_status st, const char* message) { return fail(st, "%s", message); }
+kvpop_status host_cuda_fail(int cuda_error, const char* what) {
+  return cuda_fail(static_cast<cudaError_t>(cuda_error), what);
+}
+kvpop_status host_device() {
+  DeviceInfo dev;
+  return device_info(&dev);
+}
+int32_t* host_debug_word() { return debug_word(); }
+}  // namespace kvpop
 
 extern "C" {
 

@@ -1,0 +1,578 @@
+// One decode step of attention over the paged cache, sm_100a.
+//
+//   s[g, c] = scale q[g] . K[c]     lse[g] = ln sum_c exp(s[g, c])
+//   out[g]  = sum_c exp(s[g, c] - lse[g]) V[c]
+//   weight[c] += sum_g exp(s[g, c] - lse[g])                (optional)
+//
+// K and V are read once and every byte of them takes part in 2 G to 4 G
+// multiply-adds, far below what the tensor pipe could do per byte: the bound
+// is the HBM.  So the kernel is built around its loads.  Each warp takes tiles
+// of 16 slots straight from global memory into registers, in exactly the
+// places where mma.m16n8k16 wants them, one tile ahead of the one it computes:
+//   K  is the B operand (n = key, k = head dim).  Lane (g, t) of the warp
+//      (g = lane / 4, t = lane % 4) loads 16 bytes of row g at chunk t + 4 j:
+//      the product runs over the head dim in any order, so the chunk's
+//      elements simply serve as its k indexes, and q is fetched in the same order.
+//   V  is the B operand of the second product (k = slot, n = head dim).  Lane
+//      (g, t) loads 16 bytes of rows 2t, 2t + 1, 2t + 8, 2t + 9 at chunk g; a
+//      byte permute pairs the two rows of a k pair, and n again runs over
+//      the head dim in whatever order the chunks give.
+// There is no shared memory, no barrier and no transposition on the way, and
+// a page may lie anywhere, since each group of 8 slots computes its address.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "kvpop_paged.cuh"
+
+namespace kvpop {
+
+constexpr int kPdWarps = 4;
+constexpr int kPdThreads = 32 * kPdWarps;
+constexpr int kPdTile = 16;                 // slots of one step of a warp
+constexpr int kPdMaxSplit = 2048;           // slots of one CTA at most
+constexpr int kPdMinPage = 8;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// D += A B, 16 x 8 x 16, fp32 accumulation; bf16 operands, or fp16 for an 8-bit cache.
+template <bool kF8>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (kF8)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// Two e4m3 values to two fp16 ones: exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t v;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"(static_cast<uint16_t>(two)));
+  return v;
+}
+// A pair of probabilities as a high part in the operand type and the rest as
+// a low one: 16 bits of mantissa in bf16, 22 in fp16, so the products with V,
+// which are exact in fp32, see the probability to 2^-17 or better.
+template <bool kF8>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+  if constexpr (kF8) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(a - bf_lo(hi), b - bf_hi(hi));
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+  }
+}
+
+// One tile of 16 slots in registers.
+template <int D, bool kF8>
+struct Tile {
+  static constexpr int kRow = D * (kF8 ? 1 : 2);                // bytes of a slot's K (or V)
+  static constexpr int kK = kRow / 64;                          // 16-byte chunks of a K row per lane
+  static constexpr int kV = kRow >= 128 ? kRow / 128 : 1;       // 16-byte (8-byte when a row is 64) chunks of a V row
+  uint4 k[2][kK];
+  uint4 v[4][kV];
+  int lim[2];                                                   // slots in use of each half
+};
+
+// kWide: 9 to 16 query heads per CTA, else up to 8.  With up to 8 heads the
+// lower 8 rows of the 16-row A operand are free, and the second product puts
+// the low parts of the probabilities there: both parts in one instruction.
+template <int D, bool kF8, bool kWide>
+__global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+  using T = Tile<D, kF8>;
+  constexpr int NT = D / 8;                 // 8-column tiles of out
+  constexpr int KS = D / 16;                // k steps of q . K
+  constexpr int kRows = kWide ? 16 : 8;     // query heads a CTA holds
+  constexpr float kShift = kF8 ? 8.f : 0.f; // probabilities are held times 2^kShift: fp16's small end stays out of the way
+  __shared__ int32_t pages[kPdMaxSplit / kPdMinPage + 1];
+  __shared__ float sm_m[kPdWarps][kRows], sm_l[kPdWarps][kRows];
+  __shared__ float sm_o[kPdWarps][kRows][D];
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int hc = blockIdx.x % p.head_chunks;              // chunk of 16 heads of the group
+  const int row = blockIdx.x / p.head_chunks;             // (b, h)
+  const int b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
+  const int split = blockIdx.y;
+  const int G = min(p.group - hc * 16, 16);               // query heads of this CTA
+  const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + h * p.group + hc * 16;
+  const int lo = split * p.split_slots;
+
+  grid_wait();
+  const int n = min(max(p.c.count[row], 0), p.c.capacity);
+  const int cnt = min(n - lo, p.split_slots);             // slots of this CTA
+  if (cnt <= 0) {
+    grid_launch_next();
+    for (int i = threadIdx.x; i < G; i += kPdThreads) {
+      if (p.n_split > 1) p.part_ml[(bg0 + i) * p.n_split + split] = make_float2(-INFINITY, 0.f);
+      else if (p.lse != nullptr) p.lse[bg0 + i] = -INFINITY;
+      if (p.n_split == 1 && p.scores != nullptr) p.part_ml[bg0 + i] = make_float2(-INFINITY, 0.f);
+    }
+    if (p.n_split == 1)
+      for (int i = threadIdx.x; i < G * D; i += kPdThreads) p.out[bg0 * D + i] = 0;
+    return;
+  }
+  // The pages of this CTA's slots, checked once.
+  const int e0 = lo >> p.c.page_shift;
+  const int n_ent = ((lo + cnt - 1) >> p.c.page_shift) - e0 + 1;
+  for (int i = threadIdx.x; i < n_ent; i += kPdThreads) pages[i] = page_of(p.c, b, e0 + i, p.status, DBG_PAGED_DECODE, 1);
+
+  // q in the order of K's chunks: A operand rows g and (wide) g + 8.
+  uint32_t qa[KS][kWide ? 4 : 2];
+  float qs[kWide ? 2 : 1];                                // score per unit of product, log2 units
+#pragma unroll
+  for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+    const int head = g + 8 * r;
+    const uint16_t* qr = p.q + b * p.q_stride + static_cast<int64_t>(h * p.group + hc * 16 + head) * D;
+    uint32_t x[KS][2];                                    // bf16 pairs: k step s, first and second half
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      // bf16 cache: chunk j holds dims 32 j + 8 t + 0..7, two k steps; e4m3: dims 64 j' + 16 t + 0..15, four.
+      const int d0 = kF8 ? 64 * (j / 2) + 16 * t + 8 * (j & 1) : 32 * j + 8 * t;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (head < G) w = __ldg(reinterpret_cast<const uint4*>(qr + d0));
+      x[2 * j][0] = w.x, x[2 * j][1] = w.y, x[2 * j + 1][0] = w.z, x[2 * j + 1][1] = w.w;
+    }
+    qs[r] = p.scale_log2;
+    if constexpr (kF8) {
+      // fp16 q: scaled by a power of two so that its largest entry is in [1/2, 1): exact for every entry down
+      // to 2^-14 of it, and to 2^-25 of it below.
+      float top = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) top = fmaxf(top, fmaxf(fabsf(bf_lo(x[s][i])), fabsf(bf_hi(x[s][i]))));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = 0;
+      if (top > 0.f && top < INFINITY) frexpf(top, &e);
+      e = max(-120, min(120, e));
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      qs[r] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (p.c.k_scale != nullptr ? p.c.k_scale[h] : 1.f);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const __half2 y = __floats2half2_rn(bf_lo(x[s][i]) * down, bf_hi(x[s][i]) * down);
+          x[s][i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      qa[s][r] = x[s][0];
+      qa[s][(kWide ? 2 : 1) + r] = x[s][1];
+    }
+  }
+  __syncthreads();
+
+  // Lane parts of the addresses.
+  const uint8_t* kb = p.c.k + h * p.c.k_head + g * p.c.k_slot + 16 * t;
+  const uint8_t* vb = p.c.v + h * p.c.v_head + 2 * t * p.c.v_slot + (T::kRow >= 128 ? 16 : 8) * g;
+  const int page_mask = (1 << p.c.page_shift) - 1;
+  const int tiles = (cnt + kPdTile - 1) / kPdTile;
+
+  auto fetch = [&](T& x, int tile) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int at = tile * kPdTile + 8 * half;           // slot within this CTA's range
+      int lim = min(max(cnt - at, 0), 8);
+      const int page = lim > 0 ? pages[((lo + at) >> p.c.page_shift) - e0] : -1;
+      if (page < 0) lim = 0;
+      x.lim[half] = lim;
+      if (lim > 0) {
+        const int off = (lo + at) & page_mask;
+        const uint8_t* kp = kb + page * p.c.k_page + off * p.c.k_slot;
+        const uint8_t* vp = vb + page * p.c.v_page + off * p.c.v_slot;
+#pragma unroll
+        for (int j = 0; j < T::kK; ++j) x.k[half][j] = ldg16(kp + 64 * j);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < T::kV; ++j) {
+            if constexpr (T::kRow >= 128) {
+              x.v[2 * half + r][j] = ldg16(vp + r * p.c.v_slot + 128 * j);
+            } else {
+              const uint2 w = ldg8(vp + r * p.c.v_slot);
+              x.v[2 * half + r][j] = make_uint4(w.x, w.y, 0, 0);
+            }
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < T::kK; ++j) x.k[half][j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < T::kV; ++j) x.v[2 * half + r][j] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+
+  // Running state of head rows g (0) and g + 8 (1, wide): max, this lane's part of the sum, out.
+  float m[kWide ? 2 : 1], l[kWide ? 2 : 1];
+#pragma unroll
+  for (int r = 0; r < (kWide ? 2 : 1); ++r) m[r] = -INFINITY, l[r] = 0.f;
+  float o[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+  auto compute = [&](T& x, int tile) {
+    float s[2][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[half][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < T::kK; ++j) {
+        const uint32_t w[4] = {x.k[half][j].x, x.k[half][j].y, x.k[half][j].z, x.k[half][j].w};
+        if constexpr (kF8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int st = 4 * j + i;
+            mma16<true>(s[half], qa[st][0], kWide ? qa[st][1] : 0u, qa[st][kWide ? 2 : 1], kWide ? qa[st][kWide ? 3 : 0] : 0u,
+                        e4m3x2_to_f16x2(w[i] & 0xffffu), e4m3x2_to_f16x2(w[i] >> 16));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int st = 2 * j + i;
+            mma16<false>(s[half], qa[st][0], kWide ? qa[st][1] : 0u, qa[st][kWide ? 2 : 1], kWide ? qa[st][kWide ? 3 : 0] : 0u,
+                         w[2 * i], w[2 * i + 1]);
+          }
+        }
+      }
+    }
+    // Scale, mask, and the tile's maximum over the four lanes of a head row.
+    float top[kWide ? 2 : 1];
+#pragma unroll
+    for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+      float y = -INFINITY;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& z = s[half][2 * r + e];
+          z = (2 * t + e < x.lim[half]) ? z * qs[r] : -INFINITY;
+          y = fmaxf(y, z);
+        }
+      if (p.scores != nullptr && g + 8 * r < G) {
+        float* to = p.scores + (bg0 + g + 8 * r) * p.score_pitch + lo + tile * kPdTile + 2 * t;
+        *reinterpret_cast<float2*>(to) = make_float2(s[0][2 * r], s[0][2 * r + 1]);
+        *reinterpret_cast<float2*>(to + 8) = make_float2(s[1][2 * r], s[1][2 * r + 1]);
+      }
+      y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+      y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+      top[r] = fmaxf(m[r], y);
+    }
+    bool grown = top[0] > m[0];
+    if constexpr (kWide) grown = grown || top[1] > m[1];
+    if (__any_sync(0xffffffffu, grown)) {
+      float f[kWide ? 2 : 1];
+#pragma unroll
+      for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+        f[r] = m[r] == top[r] ? 1.f : ex2(m[r] - top[r]);   // 0 for a row that had nothing yet
+        m[r] = top[r];
+        l[r] *= f[r];
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        o[i][0] *= f[0];
+        o[i][1] *= f[0];
+        o[i][2] *= f[kWide ? 1 : 0];
+        o[i][3] *= f[kWide ? 1 : 0];
+      }
+    }
+    // Probabilities, as the A operand of the second product.
+    uint32_t hi[2][kWide ? 2 : 1], low[2][kWide ? 2 : 1];
+#pragma unroll
+    for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+      const float base = (m[r] == -INFINITY ? 0.f : m[r]) - kShift;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float a = ex2(s[half][2 * r] - base), c = ex2(s[half][2 * r + 1] - base);
+        l[r] += a + c;
+        split_pair<kF8>(a, c, hi[half][r], low[half][r]);
+      }
+    }
+    // Rows past the slots in use hold anything: 0 x NaN must not reach the sums.
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      if (x.lim[half] < 8) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (2 * t + r >= x.lim[half]) {
+#pragma unroll
+            for (int j = 0; j < T::kV; ++j) x.v[2 * half + r][j] = make_uint4(0, 0, 0, 0);
+          }
+      }
+    auto second = [&](float (&c)[4], uint32_t b0, uint32_t b1) {
+      if constexpr (kWide) {
+        mma16<kF8>(c, hi[0][0], hi[0][kWide ? 1 : 0], hi[1][0], hi[1][kWide ? 1 : 0], b0, b1);
+        mma16<kF8>(c, low[0][0], low[0][kWide ? 1 : 0], low[1][0], low[1][kWide ? 1 : 0], b0, b1);
+      } else {
+        mma16<kF8>(c, hi[0][0], low[0][0], hi[1][0], low[1][0], b0, b1);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < T::kV; ++j) {
+      const uint32_t w[4][4] = {{x.v[0][j].x, x.v[0][j].y, x.v[0][j].z, x.v[0][j].w},
+                                {x.v[1][j].x, x.v[1][j].y, x.v[1][j].z, x.v[1][j].w},
+                                {x.v[2][j].x, x.v[2][j].y, x.v[2][j].z, x.v[2][j].w},
+                                {x.v[3][j].x, x.v[3][j].y, x.v[3][j].z, x.v[3][j].w}};
+      if constexpr (kF8) {
+#pragma unroll
+        for (int i = 0; i < (T::kRow >= 128 ? 4 : 2); ++i) {
+          const uint32_t x0 = __byte_perm(w[0][i], w[1][i], 0x5140), x1 = __byte_perm(w[2][i], w[3][i], 0x5140);
+          const uint32_t y0 = __byte_perm(w[0][i], w[1][i], 0x7362), y1 = __byte_perm(w[2][i], w[3][i], 0x7362);
+          second(o[4 * i], e4m3x2_to_f16x2(x0 & 0xffffu), e4m3x2_to_f16x2(x1 & 0xffffu));
+          second(o[4 * i + 1], e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(x1 >> 16));
+          second(o[4 * i + 2], e4m3x2_to_f16x2(y0 & 0xffffu), e4m3x2_to_f16x2(y1 & 0xffffu));
+          second(o[4 * i + 3], e4m3x2_to_f16x2(y0 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          second(o[8 * j + 2 * i], __byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x5410));
+          second(o[8 * j + 2 * i + 1], __byte_perm(w[0][i], w[1][i], 0x7632), __byte_perm(w[2][i], w[3][i], 0x7632));
+        }
+      }
+    }
+  };
+
+  // One tile in flight while the other is computed.
+  T buf[2];
+  if (warp < tiles) fetch(buf[0], warp);
+  for (int tile = warp; tile < tiles; tile += 2 * kPdWarps) {
+    if (tile + kPdWarps < tiles) fetch(buf[1], tile + kPdWarps);
+    compute(buf[0], tile);
+    if (tile + kPdWarps < tiles) {
+      if (tile + 2 * kPdWarps < tiles) fetch(buf[0], tile + 2 * kPdWarps);
+      compute(buf[1], tile + kPdWarps);
+    }
+  }
+  grid_launch_next();
+
+  // Join the warps: every lane holds part of its rows' sums, all four lanes of a row the same maximum.
+#pragma unroll
+  for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    if (t == 0) {
+      sm_m[warp][g + 8 * r] = m[r];
+      sm_l[warp][g + 8 * r] = l[r];
+    }
+  }
+  // Column n of out tile i is a head dim that follows from V's chunks: bf16: 64 (i / 8) + 8 n + i % 8;
+  // e4m3: (d / 8) n + i.  This lane holds n = 2 t and 2 t + 1.
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = kF8 ? (D / 8) * (2 * t + e) + i : 64 * (i / 8) + 8 * (2 * t + e) + (i % 8);
+      if constexpr (kWide) {
+        sm_o[warp][g][col] = o[i][e];
+        sm_o[warp][g + 8][col] = o[i][2 + e];
+      } else {
+        sm_o[warp][g][col] = o[i][e] + o[i][2 + e];
+      }
+    }
+  __syncthreads();
+  const float vs = kF8 && p.c.v_scale != nullptr ? p.c.v_scale[h] : 1.f;
+  for (int idx = threadIdx.x; idx < G * D; idx += kPdThreads) {
+    const int i = idx / D, d = idx - i * D;
+    float top = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPdWarps; ++w) top = fmaxf(top, sm_m[w][i]);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < kPdWarps; ++w) {
+      const float f = ex2(sm_m[w][i] - base);
+      sum += sm_l[w][i] * f;
+      acc += sm_o[w][i][d] * f;
+    }
+    const int64_t bg = bg0 + i;
+    if (p.n_split == 1) {
+      const __nv_bfloat16 y = __float2bfloat16_rn(sum != 0.f ? acc / sum * vs : 0.f);
+      p.out[bg * D + d] = *reinterpret_cast<const uint16_t*>(&y);
+      if (d == 0) {
+        if (p.lse != nullptr) p.lse[bg] = sum != 0.f ? (top - kShift + log2f(sum)) * kLn2 : -INFINITY;
+        if (p.scores != nullptr) p.part_ml[bg] = make_float2(top - kShift, sum);
+      }
+    } else {
+      p.part_o[(bg * p.n_split + split) * D + d] = acc * vs;
+      if (d == 0) p.part_ml[bg * p.n_split + split] = make_float2(top - kShift, sum);
+    }
+  }
+}
+
+// Joins the splits of a row and adds the probabilities to the weights: CTAs
+// 0 .. B H_q - 1 write out and lse of one query head each, the rest take
+// kPjSlots slots of one (b, h) row.
+constexpr int kPjThreads = 128;
+constexpr int kPjSlots = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr int kParts = kPjThreads / (D / 4);             // splits read side by side
+  __shared__ float4 acc_s[kParts][D / 4];
+  __shared__ float red[kPjThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int outs = p.n_split > 1 ? p.c.batch * p.n_q_heads : 0;
+  grid_wait();
+  grid_launch_next();
+  const int ns = p.n_split;
+  if (static_cast<int>(blockIdx.x) < outs) {
+    const int64_t bg = blockIdx.x;
+    const float2* ml = p.part_ml + bg * ns;
+    float top = -INFINITY;
+    for (int i = tid; i < ns; i += kPjThreads) top = fmaxf(top, ml[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPjThreads / 32; ++w) top = fmaxf(top, red[w]);
+    const float base = top == -INFINITY ? 0.f : top;
+    const int c = tid % (D / 4), part = tid / (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = part; i < ns; i += kParts) {
+      const float2 x = ml[i];
+      if (x.x == -INFINITY && x.y == 0.f) continue;        // nothing written for an empty split
+      const float f = ex2(x.x - base);
+      const float4 y = *reinterpret_cast<const float4*>(p.part_o + (bg * ns + i) * D + 4 * c);
+      sum += x.y * f;
+      acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
+    }
+    acc_s[part][c] = acc;
+    __shared__ float sums[kParts];
+    if (c == 0) sums[part] = sum;
+    __syncthreads();
+    if (part == 0) {
+      float total = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        total += sums[i];
+        y.x += acc_s[i][c].x, y.y += acc_s[i][c].y, y.z += acc_s[i][c].z, y.w += acc_s[i][c].w;
+      }
+      const float inv = total != 0.f ? 1.f / total : 0.f;
+      const __nv_bfloat162 u = __floats2bfloat162_rn(total != 0.f ? y.x * inv : 0.f, total != 0.f ? y.y * inv : 0.f);
+      const __nv_bfloat162 w = __floats2bfloat162_rn(total != 0.f ? y.z * inv : 0.f, total != 0.f ? y.w * inv : 0.f);
+      *reinterpret_cast<uint2*>(p.out + bg * D + 4 * c) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
+      if (c == 0 && p.lse != nullptr) p.lse[bg] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
+    }
+    return;
+  }
+  // weight[c] += sum over the group of 2^(s - lse2): the row's lse from its splits, one warp per head.
+  const int chunks = (p.c.capacity + kPjSlots - 1) / kPjSlots;
+  const int id = static_cast<int>(blockIdx.x) - outs;
+  const int row = id / chunks, chunk = id - row * chunks;
+  const int b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
+  const int n = min(max(p.c.count[row], 0), p.c.capacity);
+  const int first = chunk * kPjSlots;
+  if (first >= n) return;
+  const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + static_cast<int64_t>(h) * p.group;
+  __shared__ float lse2[64];
+  float add[kPjSlots / kPjThreads] = {};
+  for (int g0 = 0; g0 < p.group; g0 += 64) {
+    const int gn = min(64, p.group - g0);
+    __syncthreads();
+    for (int i = warp; i < gn; i += kPjThreads / 32) {
+      const float2* ml = p.part_ml + (bg0 + g0 + i) * ns;
+      float top = -INFINITY, sum = 0.f;
+      for (int s = lane; s < ns; s += 32) top = fmaxf(top, ml[s].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float base = top == -INFINITY ? 0.f : top;
+      for (int s = lane; s < ns; s += 32) sum += ml[s].y * ex2(ml[s].x - base);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) lse2[i] = sum != 0.f ? base + log2f(sum) : INFINITY;      // nothing to add: 2^-inf
+    }
+    __syncthreads();
+    for (int i = 0; i < gn; ++i) {
+      const float* s = p.scores + (bg0 + g0 + i) * p.score_pitch;
+#pragma unroll
+      for (int u = 0; u < kPjSlots / kPjThreads; ++u) {
+        const int at = first + u * kPjThreads + tid;
+        if (at < n) add[u] += ex2(s[at] - lse2[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kPjSlots / kPjThreads; ++u) {
+    const int at = first + u * kPjThreads + tid;
+    if (at >= n) continue;
+    const int page = page_of(p.c, b, at >> p.c.page_shift, nullptr, DBG_PAGED_JOIN, 1);   // reported by the attention
+    if (page < 0) continue;
+    const int64_t to = ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) + (at & ((1 << p.c.page_shift) - 1));
+    p.c.weight[to] += add[u];
+  }
+}
+
+// Slots per CTA: enough CTAs for several rounds of two per SM, so that rows
+// of different length even out, and pieces of 128 to 2048 slots.
+int paged_split_slots(int64_t rows, int capacity) {
+  constexpr int64_t kCtas = 148 * 2 * 5;
+  int64_t slots = (rows * capacity + kCtas - 1) / kCtas;
+  slots = std::max<int64_t>(128, std::min<int64_t>(kPdMaxSplit, (slots + 63) / 64 * 64));
+  return static_cast<int>(slots);
+}
+
+template <int D, bool kF8>
+static cudaError_t launch_decode_of(const PagedDecodeParams& p, int64_t rows, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(rows), p.n_split), block(kPdThreads);
+  cudaError_t e = p.group > 8 ? launch_paged(paged_decode_kernel<D, kF8, true>, grid, block, 0, 1, stream, p)
+                              : launch_paged(paged_decode_kernel<D, kF8, false>, grid, block, 0, 1, stream, p);
+  if (e != cudaSuccess || (p.n_split == 1 && p.scores == nullptr)) return e;
+  int64_t join = p.n_split > 1 ? static_cast<int64_t>(p.c.batch) * p.n_q_heads : 0;
+  if (p.scores != nullptr)
+    join += static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads * ((p.c.capacity + kPjSlots - 1) / kPjSlots);
+  return launch_paged(paged_join_kernel<D>, dim3(static_cast<unsigned>(join)), dim3(kPjThreads), 0, 1, stream, p);
+}
+
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, int head_dim, bool f8, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads * p.head_chunks;
+  if (head_dim == 128) return f8 ? launch_decode_of<128, true>(p, rows, stream) : launch_decode_of<128, false>(p, rows, stream);
+  return f8 ? launch_decode_of<64, true>(p, rows, stream) : launch_decode_of<64, false>(p, rows, stream);
+}
+
+}  // namespace kvpop
