@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kvpop_debug.cuh"
 #include "kvpop_sched.h"
 
@@ -143,6 +145,20 @@ __device__ __forceinline__ void copy_rows(const PagedView& c, const uint16_t* k,
       }
     }
   }
+}
+
+// Raises a kernel's dynamic shared memory limit on the current device, once per device (`done`: one bit each).
+// Another thread may do it again at the same time: that changes nothing.
+template <class Kern>
+static cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Launch as a programmatic dependent of the stream's previous kernel, with

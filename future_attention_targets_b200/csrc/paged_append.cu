@@ -311,19 +311,20 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
   const bool chunk = !p.one_each;
   const size_t smem = chunk ? static_cast<size_t>(p.slice) * 8 : 0;
   const dim3 grid(static_cast<unsigned>(rows * ctas)), block(kPaThreads);
-  auto go = [&](auto kern) {
+  static std::atomic<uint64_t> ready[4];
+  auto go = [&](auto kern, int which) {
     if (smem > 0) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPaMaxSlice * 8);
+      const cudaError_t e = allow_smem(kern, kPaMaxSlice * 8, ready[which]);
       if (e != cudaSuccess) return e;
     }
     return launch_paged(kern, grid, block, smem, ctas, stream, p);
   };
   if (head_dim == 128) {
-    if (f8) return chunk ? go(paged_append_kernel<128, true, true>) : go(paged_append_kernel<128, true, false>);
-    return chunk ? go(paged_append_kernel<128, false, true>) : go(paged_append_kernel<128, false, false>);
+    if (f8) return chunk ? go(paged_append_kernel<128, true, true>, 0) : go(paged_append_kernel<128, true, false>, 0);
+    return chunk ? go(paged_append_kernel<128, false, true>, 1) : go(paged_append_kernel<128, false, false>, 1);
   }
-  if (f8) return chunk ? go(paged_append_kernel<64, true, true>) : go(paged_append_kernel<64, true, false>);
-  return chunk ? go(paged_append_kernel<64, false, true>) : go(paged_append_kernel<64, false, false>);
+  if (f8) return chunk ? go(paged_append_kernel<64, true, true>, 2) : go(paged_append_kernel<64, true, false>, 2);
+  return chunk ? go(paged_append_kernel<64, false, true>, 3) : go(paged_append_kernel<64, false, false>, 3);
 }
 
 }  // namespace kvpop

@@ -6,19 +6,24 @@
 //
 // K and V are read once and every byte of them takes part in 2 G to 4 G
 // multiply-adds, far below what the tensor pipe could do per byte: the bound
-// is the HBM.  So the kernel is built around its loads.  Each warp takes tiles
-// of 16 slots straight from global memory into registers, in exactly the
-// places where mma.m16n8k16 wants them, one tile ahead of the one it computes:
+// is the HBM, and what counts is bytes in flight.  So each warp keeps a ring
+// of tiles of 16 slots in shared memory, filled by 16-byte asynchronous copies
+// several tiles ahead of the one it computes, with no barrier between warps;
+// since every 8 slots compute their own address, a page may lie anywhere and
+// rows may have any stride.
+//
+// The fragments of mma.m16n8k16 are read with plain 16-byte loads, because
+// the product does not care in which order its inner indexes run:
 //   K  is the B operand (n = key, k = head dim).  Lane (g, t) of the warp
-//      (g = lane / 4, t = lane % 4) loads 16 bytes of row g at chunk t + 4 j:
-//      the product runs over the head dim in any order, so the chunk's
-//      elements simply serve as its k indexes, and q is fetched in the same order.
+//      (g = lane / 4, t = lane % 4) reads 16 bytes of row g at chunk t + 4 j;
+//      the chunk's elements serve as its k indexes, and q is fetched in the
+//      same order.
 //   V  is the B operand of the second product (k = slot, n = head dim).  Lane
-//      (g, t) loads 16 bytes of rows 2t, 2t + 1, 2t + 8, 2t + 9 at chunk g; a
-//      byte permute pairs the two rows of a k pair, and n again runs over
-//      the head dim in whatever order the chunks give.
-// There is no shared memory, no barrier and no transposition on the way, and
-// a page may lie anywhere, since each group of 8 slots computes its address.
+//      (g, t) reads 16 bytes of rows 2t, 2t + 1, 2t + 8, 2t + 9 at chunk g; a
+//      byte permute pairs the two rows of a k pair, and n runs over the head
+//      dim in whatever order the chunks give.
+// Chunk c of row r lies at c ^ (r & 6) ^ 4 (r & 1): both patterns touch every
+// bank once per 8 lanes.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -30,21 +35,26 @@ namespace kvpop {
 
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
-constexpr int kPdTile = 16;                 // slots of one step of a warp
 constexpr int kPdMaxSplit = 2048;           // slots of one CTA at most
 constexpr int kPdMinPage = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+__device__ __forceinline__ void copy16(uint32_t smem, const uint8_t* p) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -97,16 +107,26 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
   }
 }
 
-// One tile of 16 slots in registers.
+// A tile in shared memory: K rows, then V rows.  Rows of 256 bytes come 16 at a
+// time, shorter ones 32: a step's chain of products, maximum, exponentials and
+// products costs about the same either way, and an e4m3 cache with half the
+// bytes per slot was bound by that chain (32 x 8 x 8,192 slots: 66.8 us with
+// 16, (see below) us with 32).
 template <int D, bool kF8>
 struct Tile {
   static constexpr int kRow = D * (kF8 ? 1 : 2);                // bytes of a slot's K (or V)
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kSlots = kRow == 256 ? 16 : 32;
+  static constexpr int kH = kSlots / 8;                         // groups of 8 slots, each on one page
+  static constexpr int kBytes = 2 * kSlots * kRow;
   static constexpr int kK = kRow / 64;                          // 16-byte chunks of a K row per lane
   static constexpr int kV = kRow >= 128 ? kRow / 128 : 1;       // 16-byte (8-byte when a row is 64) chunks of a V row
-  uint4 k[2][kK];
-  uint4 v[4][kV];
-  int lim[2];                                                   // slots in use of each half
+  static constexpr int kStages = kRow == 64 ? 6 : 3;
+  static constexpr int kRing = kStages * kBytes;                // bytes of a warp's ring
 };
+
+// Chunk permutation of row r within a tile.
+__device__ __forceinline__ int swizzle(int r) { return (r & 6) ^ ((r & 1) << 2); }
 
 // kWide: 9 to 16 query heads per CTA, else up to 8.  With up to 8 heads the
 // lower 8 rows of the 16-row A operand are free, and the second product puts
@@ -120,7 +140,9 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
   constexpr float kShift = kF8 ? 8.f : 0.f; // probabilities are held times 2^kShift: fp16's small end stays out of the way
   __shared__ int32_t pages[kPdMaxSplit / kPdMinPage + 1];
   __shared__ float sm_m[kPdWarps][kRows], sm_l[kPdWarps][kRows];
-  __shared__ float sm_o[kPdWarps][kRows][D];
+  extern __shared__ __align__(128) uint8_t rings[];
+  float (*sm_o)[kRows][D] = reinterpret_cast<float (*)[kRows][D]>(rings);   // once the rings are done with
+  static_assert(kRows * D * 4 <= T::kRing, "the warps' outputs reuse their rings");
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -199,44 +221,41 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
   }
   __syncthreads();
 
-  // Lane parts of the addresses.
-  const uint8_t* kb = p.c.k + h * p.c.k_head + g * p.c.k_slot + 16 * t;
-  const uint8_t* vb = p.c.v + h * p.c.v_head + 2 * t * p.c.v_slot + (T::kRow >= 128 ? 16 : 8) * g;
+  // Lane parts of the addresses: 32 lanes copy kRowsPer rows at a time, a chunk each.
+  constexpr int kRowsPer = 32 / T::kChunks;
+  constexpr int kSwz = T::kChunks >= 8 ? 7 : 3;           // a 64-byte row has four chunks to permute
+  const int row_l = lane / T::kChunks, chunk_l = lane % T::kChunks;
+  const uint8_t* kb = p.c.k + h * p.c.k_head + row_l * p.c.k_slot + 16 * chunk_l;
+  const uint8_t* vb = p.c.v + h * p.c.v_head + row_l * p.c.v_slot + 16 * chunk_l;
   const int page_mask = (1 << p.c.page_shift) - 1;
-  const int tiles = (cnt + kPdTile - 1) / kPdTile;
+  const int tiles = (cnt + T::kSlots - 1) / T::kSlots;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(rings)) + warp * T::kRing;
 
-  auto fetch = [&](T& x, int tile) {
+  // Slots in use of each half of a tile (0 for one on a bad page).
+  auto limits = [&](int tile, int half) {
+    const int at = tile * T::kSlots + 8 * half;             // slot within this CTA's range
+    const int lim = min(max(cnt - at, 0), 8);
+    return lim > 0 && pages[((lo + at) >> p.c.page_shift) - e0] >= 0 ? lim : 0;
+  };
+  // Starts the copies of a tile.  A half in use is copied whole (its page holds 8 rows), one that is not stays as it
+  // is in the ring.
+  auto fetch = [&](int tile, int stage) {
+    const uint32_t to = ring + stage * T::kBytes;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int at = tile * kPdTile + 8 * half;           // slot within this CTA's range
-      int lim = min(max(cnt - at, 0), 8);
-      const int page = lim > 0 ? pages[((lo + at) >> p.c.page_shift) - e0] : -1;
-      if (page < 0) lim = 0;
-      x.lim[half] = lim;
-      if (lim > 0) {
-        const int off = (lo + at) & page_mask;
-        const uint8_t* kp = kb + page * p.c.k_page + off * p.c.k_slot;
-        const uint8_t* vp = vb + page * p.c.v_page + off * p.c.v_slot;
+    for (int half = 0; half < T::kH; ++half) {
+      const int at = tile * T::kSlots + 8 * half;
+      if (at >= cnt) break;
+      const int page = pages[((lo + at) >> p.c.page_shift) - e0];
+      if (page < 0) continue;
+      const int off = (lo + at) & page_mask;
+      const uint8_t* kp = kb + page * p.c.k_page + off * p.c.k_slot;
+      const uint8_t* vp = vb + page * p.c.v_page + off * p.c.v_slot;
 #pragma unroll
-        for (int j = 0; j < T::kK; ++j) x.k[half][j] = ldg16(kp + 64 * j);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < T::kV; ++j) {
-            if constexpr (T::kRow >= 128) {
-              x.v[2 * half + r][j] = ldg16(vp + r * p.c.v_slot + 128 * j);
-            } else {
-              const uint2 w = ldg8(vp + r * p.c.v_slot);
-              x.v[2 * half + r][j] = make_uint4(w.x, w.y, 0, 0);
-            }
-          }
-      } else {
-#pragma unroll
-        for (int j = 0; j < T::kK; ++j) x.k[half][j] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < T::kV; ++j) x.v[2 * half + r][j] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < (8 + kRowsPer - 1) / kRowsPer; ++i) {
+        const int r = 8 * half + i * kRowsPer + row_l;
+        const uint32_t dst = to + r * T::kRow + 16 * (chunk_l ^ (swizzle(r) & kSwz));
+        copy16(dst, kp + i * kRowsPer * p.c.k_slot);
+        copy16(dst + T::kSlots * T::kRow, vp + i * kRowsPer * p.c.v_slot);
       }
     }
   };
@@ -251,15 +270,20 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-  auto compute = [&](T& x, int tile) {
-    float s[2][4];
+  auto compute = [&](int tile, int stage) {
+    const uint32_t kt = ring + stage * T::kBytes, vt = kt + T::kSlots * T::kRow;
+    int lim[T::kH];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < T::kH; ++half) lim[half] = limits(tile, half);
+    float s[T::kH][4];
+#pragma unroll
+    for (int half = 0; half < T::kH; ++half) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[half][e] = 0.f;
 #pragma unroll
       for (int j = 0; j < T::kK; ++j) {
-        const uint32_t w[4] = {x.k[half][j].x, x.k[half][j].y, x.k[half][j].z, x.k[half][j].w};
+        const uint4 kx = lds16(kt + (8 * half + g) * T::kRow + 16 * ((t + 4 * j) ^ (swizzle(g) & kSwz)));
+        const uint32_t w[4] = {kx.x, kx.y, kx.z, kx.w};
         if constexpr (kF8) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -283,17 +307,18 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
     for (int r = 0; r < (kWide ? 2 : 1); ++r) {
       float y = -INFINITY;
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int half = 0; half < T::kH; ++half)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float& z = s[half][2 * r + e];
-          z = (2 * t + e < x.lim[half]) ? z * qs[r] : -INFINITY;
+          z = (2 * t + e < lim[half]) ? z * qs[r] : -INFINITY;
           y = fmaxf(y, z);
         }
       if (p.scores != nullptr && g + 8 * r < G) {
-        float* to = p.scores + (bg0 + g + 8 * r) * p.score_pitch + lo + tile * kPdTile + 2 * t;
-        *reinterpret_cast<float2*>(to) = make_float2(s[0][2 * r], s[0][2 * r + 1]);
-        *reinterpret_cast<float2*>(to + 8) = make_float2(s[1][2 * r], s[1][2 * r + 1]);
+        float* to = p.scores + (bg0 + g + 8 * r) * p.score_pitch + lo + tile * T::kSlots + 2 * t;
+#pragma unroll
+        for (int half = 0; half < T::kH; ++half)
+          *reinterpret_cast<float2*>(to + 8 * half) = make_float2(s[half][2 * r], s[half][2 * r + 1]);
       }
       y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
       y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
@@ -318,74 +343,83 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
       }
     }
     // Probabilities, as the A operand of the second product.
-    uint32_t hi[2][kWide ? 2 : 1], low[2][kWide ? 2 : 1];
+    uint32_t hi[T::kH][kWide ? 2 : 1], low[T::kH][kWide ? 2 : 1];
 #pragma unroll
     for (int r = 0; r < (kWide ? 2 : 1); ++r) {
       const float base = (m[r] == -INFINITY ? 0.f : m[r]) - kShift;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int half = 0; half < T::kH; ++half) {
         const float a = ex2(s[half][2 * r] - base), c = ex2(s[half][2 * r + 1] - base);
         l[r] += a + c;
         split_pair<kF8>(a, c, hi[half][r], low[half][r]);
       }
     }
-    // Rows past the slots in use hold anything: 0 x NaN must not reach the sums.
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-      if (x.lim[half] < 8) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (2 * t + r >= x.lim[half]) {
-#pragma unroll
-            for (int j = 0; j < T::kV; ++j) x.v[2 * half + r][j] = make_uint4(0, 0, 0, 0);
-          }
-      }
-    auto second = [&](float (&c)[4], uint32_t b0, uint32_t b1) {
+    auto second = [&](float (&c)[4], int kk, uint32_t b0, uint32_t b1) {
       if constexpr (kWide) {
-        mma16<kF8>(c, hi[0][0], hi[0][kWide ? 1 : 0], hi[1][0], hi[1][kWide ? 1 : 0], b0, b1);
-        mma16<kF8>(c, low[0][0], low[0][kWide ? 1 : 0], low[1][0], low[1][kWide ? 1 : 0], b0, b1);
+        mma16<kF8>(c, hi[kk][0], hi[kk][kWide ? 1 : 0], hi[kk + 1][0], hi[kk + 1][kWide ? 1 : 0], b0, b1);
+        mma16<kF8>(c, low[kk][0], low[kk][kWide ? 1 : 0], low[kk + 1][0], low[kk + 1][kWide ? 1 : 0], b0, b1);
       } else {
-        mma16<kF8>(c, hi[0][0], low[0][0], hi[1][0], low[1][0], b0, b1);
+        mma16<kF8>(c, hi[kk][0], low[kk][0], hi[kk + 1][0], low[kk + 1][0], b0, b1);
       }
     };
 #pragma unroll
+    for (int kk = 0; kk < T::kH; kk += 2)
+#pragma unroll
     for (int j = 0; j < T::kV; ++j) {
-      const uint32_t w[4][4] = {{x.v[0][j].x, x.v[0][j].y, x.v[0][j].z, x.v[0][j].w},
-                                {x.v[1][j].x, x.v[1][j].y, x.v[1][j].z, x.v[1][j].w},
-                                {x.v[2][j].x, x.v[2][j].y, x.v[2][j].z, x.v[2][j].w},
-                                {x.v[3][j].x, x.v[3][j].y, x.v[3][j].z, x.v[3][j].w}};
+      // Rows 2t, 2t + 1, 2t + 8, 2t + 9.  Rows past the slots in use hold anything: 0 x NaN must not reach the sums.
+      uint32_t w[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int in_half = 2 * t + (r & 1), rr = 8 * (kk + (r >> 1)) + in_half;
+        uint4 vx = make_uint4(0, 0, 0, 0);
+        if constexpr (T::kRow >= 128) {
+          vx = lds16(vt + rr * T::kRow + 16 * ((g + 8 * j) ^ swizzle(in_half)));
+        } else {
+          const uint2 y = lds8(vt + rr * T::kRow + 16 * ((g >> 1) ^ (swizzle(in_half) & kSwz)) + 8 * (g & 1));
+          vx.x = y.x, vx.y = y.y;
+        }
+        if (in_half >= lim[kk + (r >> 1)]) vx = make_uint4(0, 0, 0, 0);
+        w[r][0] = vx.x, w[r][1] = vx.y, w[r][2] = vx.z, w[r][3] = vx.w;
+      }
       if constexpr (kF8) {
 #pragma unroll
         for (int i = 0; i < (T::kRow >= 128 ? 4 : 2); ++i) {
           const uint32_t x0 = __byte_perm(w[0][i], w[1][i], 0x5140), x1 = __byte_perm(w[2][i], w[3][i], 0x5140);
           const uint32_t y0 = __byte_perm(w[0][i], w[1][i], 0x7362), y1 = __byte_perm(w[2][i], w[3][i], 0x7362);
-          second(o[4 * i], e4m3x2_to_f16x2(x0 & 0xffffu), e4m3x2_to_f16x2(x1 & 0xffffu));
-          second(o[4 * i + 1], e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(x1 >> 16));
-          second(o[4 * i + 2], e4m3x2_to_f16x2(y0 & 0xffffu), e4m3x2_to_f16x2(y1 & 0xffffu));
-          second(o[4 * i + 3], e4m3x2_to_f16x2(y0 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+          second(o[4 * i], kk, e4m3x2_to_f16x2(x0 & 0xffffu), e4m3x2_to_f16x2(x1 & 0xffffu));
+          second(o[4 * i + 1], kk, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(x1 >> 16));
+          second(o[4 * i + 2], kk, e4m3x2_to_f16x2(y0 & 0xffffu), e4m3x2_to_f16x2(y1 & 0xffffu));
+          second(o[4 * i + 3], kk, e4m3x2_to_f16x2(y0 >> 16), e4m3x2_to_f16x2(y1 >> 16));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          second(o[8 * j + 2 * i], __byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x5410));
-          second(o[8 * j + 2 * i + 1], __byte_perm(w[0][i], w[1][i], 0x7632), __byte_perm(w[2][i], w[3][i], 0x7632));
+          second(o[8 * j + 2 * i], kk, __byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x5410));
+          second(o[8 * j + 2 * i + 1], kk, __byte_perm(w[0][i], w[1][i], 0x7632), __byte_perm(w[2][i], w[3][i], 0x7632));
         }
       }
     }
   };
 
-  // One tile in flight while the other is computed.
-  T buf[2];
-  if (warp < tiles) fetch(buf[0], warp);
-  for (int tile = warp; tile < tiles; tile += 2 * kPdWarps) {
-    if (tile + kPdWarps < tiles) fetch(buf[1], tile + kPdWarps);
-    compute(buf[0], tile);
-    if (tile + kPdWarps < tiles) {
-      if (tile + 2 * kPdWarps < tiles) fetch(buf[0], tile + 2 * kPdWarps);
-      compute(buf[1], tile + kPdWarps);
-    }
+  // kStages - 1 tiles ahead of the one that is computed.
+#pragma unroll
+  for (int i = 0; i < T::kStages - 1; ++i) {
+    if (warp + i * kPdWarps < tiles) fetch(warp + i * kPdWarps, i);
+    copy_commit();
   }
+  int stage = 0;
+  for (int tile = warp; tile < tiles; tile += kPdWarps) {
+    copy_wait<T::kStages - 2>();
+    __syncwarp();                                         // every lane's copies of this tile, and its reads of the last
+    const int ahead = tile + (T::kStages - 1) * kPdWarps;
+    if (ahead < tiles) fetch(ahead, stage == 0 ? T::kStages - 1 : stage - 1);
+    copy_commit();
+    compute(tile, stage);
+    stage = stage == T::kStages - 1 ? 0 : stage + 1;
+  }
+  copy_wait<0>();
   grid_launch_next();
+  __syncthreads();                                        // the rings are free
 
   // Join the warps: every lane holds part of its rows' sums, all four lanes of a row the same maximum.
 #pragma unroll
@@ -444,7 +478,8 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
 // 0 .. B H_q - 1 write out and lse of one query head each, the rest take
 // kPjSlots slots of one (b, h) row.
 constexpr int kPjThreads = 128;
-constexpr int kPjSlots = 512;
+constexpr int kPjSlots = 4 * kPjThreads;
+constexpr int kPjHeads = kPjThreads / 16;
 
 template <int D>
 __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
@@ -501,50 +536,66 @@ __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_con
     }
     return;
   }
-  // weight[c] += sum over the group of 2^(s - lse2): the row's lse from its splits, one warp per head.
+  // weight[c] += sum over the group of 2^(s - lse2), four slots per thread (of one page); the scores of eight heads
+  // are on their way while the warps join the splits of those heads to lse2.
   const int chunks = (p.c.capacity + kPjSlots - 1) / kPjSlots;
   const int id = static_cast<int>(blockIdx.x) - outs;
   const int row = id / chunks, chunk = id - row * chunks;
   const int b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
+  const int at = chunk * kPjSlots + 4 * tid;
+  const int page = page_of(p.c, b, at >> p.c.page_shift, nullptr, DBG_PAGED_JOIN, 1);   // reported by the attention
   const int n = min(max(p.c.count[row], 0), p.c.capacity);
-  const int first = chunk * kPjSlots;
-  if (first >= n) return;
+  if (chunk * kPjSlots >= n) return;
   const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + static_cast<int64_t>(h) * p.group;
-  __shared__ float lse2[64];
-  float add[kPjSlots / kPjThreads] = {};
-  for (int g0 = 0; g0 < p.group; g0 += 64) {
-    const int gn = min(64, p.group - g0);
+  __shared__ float lse2[kPjHeads];
+  float add[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int g0 = 0; g0 < p.group; g0 += kPjHeads) {
+    float4 s[kPjHeads];
+#pragma unroll
+    for (int i = 0; i < kPjHeads; ++i)
+      if (at < n && g0 + i < p.group)
+        s[i] = *reinterpret_cast<const float4*>(p.scores + (bg0 + g0 + i) * p.score_pitch + at);
     __syncthreads();
-    for (int i = warp; i < gn; i += kPjThreads / 32) {
-      const float2* ml = p.part_ml + (bg0 + g0 + i) * ns;
+    {
+      // 16 lanes per head.
+      const int i = tid / 16, part = tid % 16;
       float top = -INFINITY, sum = 0.f;
-      for (int s = lane; s < ns; s += 32) top = fmaxf(top, ml[s].x);
+      if (g0 + i < p.group)
+        for (int j = part; j < ns; j += 16) {
+          const float2 x = p.part_ml[(bg0 + g0 + i) * ns + j];
+          const float up = fmaxf(top, x.x), base = up == -INFINITY ? 0.f : up;
+          sum = sum * ex2(top - base) + x.y * ex2(x.x - base);
+          top = up;
+        }
+      float all = top;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float base = top == -INFINITY ? 0.f : top;
-      for (int s = lane; s < ns; s += 32) sum += ml[s].y * ex2(ml[s].x - base);
+      for (int o = 8; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+      all = all == -INFINITY ? 0.f : all;
+      sum *= ex2(top - all);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) lse2[i] = sum != 0.f ? base + log2f(sum) : INFINITY;      // nothing to add: 2^-inf
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (part == 0) lse2[i] = sum != 0.f ? all + log2f(sum) : INFINITY;   // nothing to add
     }
     __syncthreads();
-    for (int i = 0; i < gn; ++i) {
-      const float* s = p.scores + (bg0 + g0 + i) * p.score_pitch;
+    if (at < n)
 #pragma unroll
-      for (int u = 0; u < kPjSlots / kPjThreads; ++u) {
-        const int at = first + u * kPjThreads + tid;
-        if (at < n) add[u] += ex2(s[at] - lse2[i]);
-      }
-    }
+      for (int i = 0; i < kPjHeads; ++i)
+        if (g0 + i < p.group) {
+          add[0] += ex2(s[i].x - lse2[i]), add[1] += ex2(s[i].y - lse2[i]);
+          add[2] += ex2(s[i].z - lse2[i]), add[3] += ex2(s[i].w - lse2[i]);
+        }
   }
+  if (at >= n || page < 0) return;
+  float* to = p.c.weight + ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) +
+              (at & ((1 << p.c.page_shift) - 1));
+  if (at + 3 < n) {
+    float4 w = *reinterpret_cast<const float4*>(to);
+    w.x += add[0], w.y += add[1], w.z += add[2], w.w += add[3];
+    *reinterpret_cast<float4*>(to) = w;
+  } else {
 #pragma unroll
-  for (int u = 0; u < kPjSlots / kPjThreads; ++u) {
-    const int at = first + u * kPjThreads + tid;
-    if (at >= n) continue;
-    const int page = page_of(p.c, b, at >> p.c.page_shift, nullptr, DBG_PAGED_JOIN, 1);   // reported by the attention
-    if (page < 0) continue;
-    const int64_t to = ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) + (at & ((1 << p.c.page_shift) - 1));
-    p.c.weight[to] += add[u];
+    for (int e = 0; e < 3; ++e)
+      if (at + e < n) to[e] += add[e];
   }
 }
 
@@ -560,8 +611,13 @@ int paged_split_slots(int64_t rows, int capacity) {
 template <int D, bool kF8>
 static cudaError_t launch_decode_of(const PagedDecodeParams& p, int64_t rows, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(rows), p.n_split), block(kPdThreads);
-  cudaError_t e = p.group > 8 ? launch_paged(paged_decode_kernel<D, kF8, true>, grid, block, 0, 1, stream, p)
-                              : launch_paged(paged_decode_kernel<D, kF8, false>, grid, block, 0, 1, stream, p);
+  constexpr size_t smem = kPdWarps * Tile<D, kF8>::kRing;
+  static std::atomic<uint64_t> ready[2];
+  auto go = [&](auto kern, int wide) {
+    const cudaError_t e = allow_smem(kern, smem, ready[wide]);
+    return e != cudaSuccess ? e : launch_paged(kern, grid, block, smem, 1, stream, p);
+  };
+  const cudaError_t e = p.group > 8 ? go(paged_decode_kernel<D, kF8, true>, 1) : go(paged_decode_kernel<D, kF8, false>, 0);
   if (e != cudaSuccess || (p.n_split == 1 && p.scores == nullptr)) return e;
   int64_t join = p.n_split > 1 ? static_cast<int64_t>(p.c.batch) * p.n_q_heads : 0;
   if (p.scores != nullptr)
