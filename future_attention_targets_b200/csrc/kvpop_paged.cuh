@@ -88,59 +88,105 @@ __device__ __forceinline__ int32_t page_of(const PagedView& c, int32_t b, int32_
   return -1;
 }
 
-// A batch of rows to write: token l_tok[i] of the sources goes to slot l_off[i]
-// of page l_page[i]; l_page[i] < 0 is skipped.
-struct RowList {
-  int32_t* page;
-  int32_t* off;
-  int32_t* tok;
+// Rows to write, in shared memory: token `tok` of the sources (from the first one of the list on) goes to offset
+// `off` of `page`; a page < 0 is skipped.
+struct RowEntry {
+  int32_t page;
+  uint32_t off_tok;       // off | tok << 10: pages have at most 1,024 slots
 };
+__device__ __forceinline__ RowEntry row_entry(int page, int off, int tok) {
+  return {page, static_cast<uint32_t>(off) | (static_cast<uint32_t>(tok) << 10)};
+}
 
-// Copies the K and V rows of `n` list entries of head h, bf16 to bf16 or to
-// e4m3, 16 bytes of input per thread and step, kUnroll steps in flight.
+// Products of two pairs of fp32 values, each rounded once.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) { return (static_cast<uint64_t>(hi) << 32) | lo; }
+// Two fp32 values to two e4m3, nearest even, clipped to +-448; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2(uint64_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+      : "=h"(r)
+      : "f"(__uint_as_float(static_cast<uint32_t>(x >> 32))), "f"(__uint_as_float(static_cast<uint32_t>(x))));
+  return r;
+}
+
+// What a cache row's values are divided by.  Rounding to e4m3 is monotonic, so where x * low and x * high, which
+// enclose the quotient, round to the same value, the correctly rounded fp32 quotient does too; else the kernel
+// divides.  low and high are the reciprocal 2^-21 to either side (it is off by 2^-24 itself and the products by as
+// much), or the reciprocal itself for a power of two, whose quotients are exact.  A division for every element
+// bound an 8-bit cache's compaction (8 prompts, 100,003 tokens: 127 us).
+struct Divisor {
+  float scale;
+  uint64_t low, high;     // twice each
+};
+__device__ __forceinline__ Divisor divisor_of(float scale) {
+  const float inv = __frcp_rn(scale);
+  const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0u && inv >= 0x1p-126f && inv <= 0x1p126f;
+  // A reciprocal out of the normal range says nothing: enclose everything.
+  const bool odd = !(inv >= 0x1p-100f && inv <= 0x1p100f);
+  const float lo = exact ? inv : odd ? 0.f : __fmul_rn(inv, 1.f - 0x1p-21f);
+  const float hi = exact ? inv : odd ? INFINITY : __fmul_rn(inv, 1.f + 0x1p-21f);
+  const uint32_t l = __float_as_uint(lo), h = __float_as_uint(hi);
+  return {scale, pair_of(l, l), pair_of(h, h)};
+}
+__device__ __forceinline__ uint2 to_e4m3x8(const uint4& in, const Divisor& by) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t x = pair_of(w[e] << 16, w[e] & 0xffff0000u);
+    r[e] = e4m3x2(mul2(x, by.low));
+    if (r[e] != e4m3x2(mul2(x, by.high)))
+      r[e] = e4m3x2(pair_of(__float_as_uint(__fdiv_rn(__uint_as_float(w[e] << 16), by.scale)),
+                            __float_as_uint(__fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), by.scale))));
+  }
+  return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+
+// Copies the K and V rows of `n` list entries of head h, bf16 to bf16 or to e4m3.  A warp takes an entry (two with 64
+// dims) at a time, its lanes the 16-byte words of K's row, then V's, with kUnroll entries in flight.
 template <int D, bool kF8, int kThreads, int kUnroll>
 __device__ __forceinline__ void copy_rows(const PagedView& c, const uint16_t* k, const uint16_t* v,
-                                          int64_t token_stride, int h, const RowList& list, int n) {
+                                          int64_t token_stride, int h, const RowEntry* list, int n) {
   constexpr int kWords = D / 8;             // 16-byte words of a bf16 row
-  float ks = 1.f, vs = 1.f;
+  constexpr int kPer = 32 / (2 * kWords);   // entries of a warp at a time
+  constexpr int kStep = kThreads / 32 * kPer;
+  const int lane = threadIdx.x & 31;
+  const int w = lane % kWords;
+  const bool is_v = (lane / kWords) & 1;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>((is_v ? v : k) + static_cast<int64_t>(h) * D + 8 * w);
+  uint8_t* dst = (is_v ? c.v + h * c.v_head : c.k + h * c.k_head) + (kF8 ? 8 : 16) * w;
+  // The host keeps these within 32 bits, so that an address is one or two wide multiply-adds.
+  const uint32_t token_bytes = static_cast<uint32_t>(token_stride) * 2u;
+  const uint32_t page_bytes = static_cast<uint32_t>(is_v ? c.v_page : c.k_page);
+  const uint32_t slot_bytes = static_cast<uint32_t>(is_v ? c.v_slot : c.k_slot);
+  Divisor by = {};
   if constexpr (kF8) {
-    if (c.k_scale != nullptr) ks = c.k_scale[h];
-    if (c.v_scale != nullptr) vs = c.v_scale[h];
+    const float* s = is_v ? c.v_scale : c.k_scale;
+    by = divisor_of(s != nullptr ? s[h] : 1.f);
   }
-  const int total = n * 2 * kWords;
-  for (int base = threadIdx.x; base < total; base += kThreads * kUnroll) {
+  for (int base = threadIdx.x / 32 * kPer + lane / (2 * kWords); base < n; base += kStep * kUnroll) {
     uint4 buf[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int idx = base + u * kThreads;
-      const int i = idx / (2 * kWords), w = idx % kWords;
-      if (idx < total && list.page[i] >= 0) {
-        const uint16_t* src = (idx / kWords) & 1 ? v : k;
-        buf[u] = __ldg(reinterpret_cast<const uint4*>(src + list.tok[i] * token_stride + static_cast<int64_t>(h) * D + 8 * w));
-      }
+      const int i = base + u * kStep;
+      if (i < n)
+        buf[u] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(list[i].off_tok >> 10) * token_bytes));
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int idx = base + u * kThreads;
-      const int i = idx / (2 * kWords), w = idx % kWords;
-      if (idx < total && list.page[i] >= 0) {
-        const bool is_v = (idx / kWords) & 1;
-        uint8_t* dst = is_v ? c.v + list.page[i] * c.v_page + h * c.v_head + list.off[i] * c.v_slot
-                            : c.k + list.page[i] * c.k_page + h * c.k_head + list.off[i] * c.k_slot;
-        if constexpr (kF8) {
-          const float scale = is_v ? vs : ks;
-          const uint32_t in[4] = {buf[u].x, buf[u].y, buf[u].z, buf[u].w};
-          uint32_t out[2] = {0, 0};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 x = make_float2(__fdiv_rn(__uint_as_float(in[e] << 16), scale),
-                                         __fdiv_rn(__uint_as_float(in[e] & 0xffff0000u), scale));
-            // Rounds to nearest even and saturates to +-448; NaN stays NaN.
-            out[e / 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3)) << (16 * (e & 1));
-          }
-          *reinterpret_cast<uint2*>(dst + 8 * w) = make_uint2(out[0], out[1]);
-        } else {
-          *reinterpret_cast<uint4*>(dst + 16 * w) = buf[u];
+      const int i = base + u * kStep;
+      if (i < n) {
+        const RowEntry e = list[i];
+        if (e.page >= 0) {
+          uint8_t* to = dst + static_cast<uint64_t>(static_cast<uint32_t>(e.page)) * page_bytes +
+                        static_cast<uint64_t>(e.off_tok & 1023u) * slot_bytes;
+          if constexpr (kF8) *reinterpret_cast<uint2*>(to) = to_e4m3x8(buf[u], by);
+          else *reinterpret_cast<uint4*>(to) = buf[u];
         }
       }
     }

@@ -72,9 +72,12 @@ kvpop_status check_cache(const kvpop_paged_cache* c) {
   const int elt = c->dtype == KVPOP_PAGED_E4M3 ? 1 : 2;
   for (int i = 0; i < 3; ++i) {
     const int64_t s[2] = {c->k_stride[i], c->v_stride[i]};
-    for (int64_t x : s)
+    for (int64_t x : s) {
       if (x < 0 || x > (int64_t(1) << 56) || x * elt % 16 != 0)
         return fail(KVPOP_ERR_INVALID_ARG, "strides must be non-negative multiples of 16 bytes");
+      if (i != 1 && x * elt >= (int64_t(1) << 32))
+        return fail(KVPOP_ERR_UNSUPPORTED, "strides between pages and between slots must be below 4 GiB");
+    }
   }
   return KVPOP_OK;
 }
@@ -197,8 +200,9 @@ kvpop_status kvpop_paged_append_kv(const void* k_new, const void* v_new, int64_t
   if (!aligned(k_new, 16) || !aligned(v_new, 16))
     return fail(KVPOP_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
   if ((st = check_cache(cache)) != KVPOP_OK) return st;
-  if (token_stride < 0 || token_stride > (int64_t(1) << 40) || token_stride % 8 != 0)
+  if (token_stride < 0 || token_stride % 8 != 0)
     return fail(KVPOP_ERR_INVALID_ARG, "token_stride must be a non-negative multiple of 8 elements");
+  if (token_stride >= (int64_t(1) << 31)) return fail(KVPOP_ERR_UNSUPPORTED, "token_stride must be below 4 GiB");
   if (cache->pos_pages == nullptr || cache->weight_pages == nullptr || cache->seen == nullptr)
     return fail(KVPOP_ERR_INVALID_ARG, "appending needs pos_pages, weight_pages and seen");
   if (window < 0 || sinks < 0) return fail(KVPOP_ERR_INVALID_ARG, "window and sinks must be >= 0");

@@ -6,11 +6,13 @@
 // 64-bit key, smaller = evicted earlier: the order-preserving bits of the
 // weight (NaN lowest), then 2^31 - 1 - position; slots that may not go (sinks,
 // recent tokens) have the key 2^64 - 1.  One token in, one out (the steady
-// state of decoding) is an argmin over the keys.  Several out is an exact
-// radix select of the e-th smallest key, digit by digit, over keys in shared
-// memory: the cluster adds its histograms through distributed shared memory,
-// and stops as soon as a digit's bucket is taken whole.  Everything is
-// integer, so the result is exact and does not depend on any order.
+// state of decoding) is an argmin over the keys, bound by the bytes of weights
+// and positions.  Several out is an exact radix select of the e-th smallest
+// key over keys in shared memory, in digits of 11 bits (a weight's first
+// digit is its exponent and two bits more, which spreads real weights over
+// many counters): the cluster adds its histograms through distributed shared
+// memory, and stops as soon as a digit's bucket is taken whole, mostly after
+// two.  Everything is integer, so the result is exact and depends on no order.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -21,31 +23,38 @@ namespace kvpop {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPaThreads = 256;
-constexpr int kPaWarps = kPaThreads / 32;
 constexpr int kPaMaxSlice = 16384;     // keys one CTA holds at most (128 KiB); 8 x 16384 = the largest capacity
+constexpr int append_threads(bool chunk) { return chunk ? 512 : 256; }
+constexpr int kPaBits = 11;           // of a digit
+constexpr int kPaBins = 1 << kPaBits;
+constexpr int kPaList = 2 * kPaBins * 4 / static_cast<int>(sizeof(RowEntry));   // as the two histograms
 constexpr uint64_t kStays = ~0ull;
 
-// Larger float -> larger key; -0 equals +0; NaN -> 0, below every number.
+// Larger float -> larger key; -0 equals +0 (the addition makes it +0); NaN -> 0, below every number.
 __device__ __forceinline__ uint32_t weight_key(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
-  if (u == 0x80000000u) u = 0u;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  f = __fadd_rn(f, 0.f);
+  const uint32_t u = __float_as_uint(f);
+  const uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return f != f ? 0u : key;
 }
 
 template <int D, bool kF8, bool kChunk>
-__global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+__global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
+    paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+  constexpr int kPaThreads = append_threads(kChunk), kPaWarps = kPaThreads / 32;
   cg::cluster_group cluster = cg::this_cluster();
   const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  extern __shared__ uint64_t keys[];                     // kChunk: this CTA's slice
+  extern __shared__ __align__(16) uint64_t keys[];       // kChunk: this CTA's slice; then the rows to write
   __shared__ uint64_t best_key[kPaWarps + 1];            // one out: minimum of each warp; [kPaWarps] = of the CTA
   __shared__ int32_t best_slot[kPaWarps + 1];
-  __shared__ uint32_t hist[2][256];                      // kChunk: a pass's histogram, read by the cluster
+  __shared__ __align__(16) uint32_t hist[kChunk ? 2 : 1][kChunk ? kPaBins : 4];   // a pass's histogram, read by the cluster
+  __shared__ __align__(16) uint32_t vary[2][4];          // AND and OR of a pass's keys, high and low halves
+  __shared__ uint64_t every_any[2];                      // the same of the whole cluster
   __shared__ uint32_t sel[3];
-  __shared__ uint32_t taken_here;                        // kChunk: victims in this slice, read by the cluster
+  __shared__ uint32_t ranks[3];                          // victims before this slice, victims in all, undecided before it
+  __shared__ uint32_t taken_here[2];                     // kChunk: victims and undecided in this slice, read by the cluster
   __shared__ uint32_t warp_sum[kPaWarps];
-  __shared__ int32_t l_page[kPaThreads], l_off[kPaThreads], l_tok[kPaThreads];
+  __shared__ RowEntry one;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / ctas, b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
@@ -62,19 +71,23 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const __grid_c
     return;
   }
   const int cap = p.c.capacity, n = min(count, cap), f = min(m, cap - n), e = m - f;
-  // Position below which a token has left the recent window once the new ones are in.
+  // Tokens at positions sinks .. recent - 1 may go: recent is where the window begins once the new ones are in.
   const int64_t recent = static_cast<int64_t>(seen) + m - p.window;
+  const uint32_t span = static_cast<uint32_t>(max(int64_t(0), min(recent, int64_t(1) << 31) - p.sinks));
   const int s0 = min(n, cta * p.slice), s1 = min(n, s0 + p.slice);
+  const uint16_t* k_src = p.k_new + tok0 * p.token_stride;
+  const uint16_t* v_src = p.v_new + tok0 * p.token_stride;
 
   auto meta_at = [&](int page, int off) {
     return ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) + off;
   };
   auto key_of = [&](float w, int pos) {
-    const bool goes = pos >= p.sinks && pos < recent;
+    // pos < 0 wraps to a large number that no span reaches.
+    const bool goes = pos >= 0 && static_cast<uint32_t>(pos) - static_cast<uint32_t>(p.sinks) < span && pos >= p.sinks;
     return goes ? (static_cast<uint64_t>(weight_key(w)) << 32) | static_cast<uint32_t>(0x7fffffff - pos) : kStays;
   };
-  // Calls use(slot, key) for the slots of this CTA's slice, 4 per thread and step (a page has at least 8 slots
-  // and slices are multiples of 8, so four slots share a page and an aligned 16 bytes).
+  // Calls use(slot, keys) for the slots of this CTA's slice, 4 per thread and step (a page has at least 8 slots and
+  // slices are multiples of 8, so four slots share a page and an aligned 16 bytes).
   auto for_keys = [&](auto&& use) {
     constexpr int kU = 4;
     for (int base = s0 + 4 * tid; base < s1; base += 4 * kPaThreads * kU) {
@@ -105,10 +118,9 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const __grid_c
       }
     }
   };
-  // Writes list entry `at`: token i of the sequence into `slot` (< 0: none for it).
-  auto place = [&](int at, int i, int slot) {
+  // Token i of the sequence into `slot` (< 0: none for it), where position `old` goes (-1: nothing does).
+  auto place = [&](int i, int slot, int old) {
     int page = -1, off = 0;
-    int32_t out = -2;
     if (slot >= 0) {
       page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 2);
       off = slot & page_mask;
@@ -117,21 +129,15 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const __grid_c
     }
     if (page >= 0) {
       const int64_t to = meta_at(page, off);
-      out = slot < n ? p.c.pos[to] : -1;
       p.c.pos[to] = seen + i;
       p.c.weight[to] = 0.f;
     }
-    if (p.evicted != nullptr) p.evicted[static_cast<int64_t>(tok0 + i) * p.c.n_kv_heads + h] = out;
-    l_page[at] = page;
-    l_off[at] = off;
-    l_tok[at] = tok0 + i;
-  };
-  auto copy = [&](int entries) {
-    copy_rows<D, kF8, kPaThreads, 4>(p.c, p.k_new, p.v_new, p.token_stride, h, {l_page, l_off, l_tok}, entries);
+    if (p.evicted != nullptr) p.evicted[static_cast<int64_t>(tok0 + i) * p.c.n_kv_heads + h] = page >= 0 ? old : -2;
+    return row_entry(page, off, i);
   };
 
   if constexpr (!kChunk) {
-    int slot = n;                                        // the free slot, if there is one
+    int slot = n, old = -1;                              // the free slot, if there is one
     if (e > 0) {
       uint64_t key = kStays;
       int at = -1;
@@ -146,72 +152,153 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const __grid_c
       }
       if (lane == 0) best_key[warp] = key, best_slot[warp] = at;
       __syncthreads();
-      if (tid == 0) {
-        for (int w = 1; w < kPaWarps; ++w)
-          if (best_key[w] < key || (best_key[w] == key && best_slot[w] < at)) key = best_key[w], at = best_slot[w];
-        best_key[kPaWarps] = key;
-        best_slot[kPaWarps] = at;
+      if (warp == 0) {
+        key = lane < kPaWarps ? best_key[lane] : kStays;
+        at = lane < kPaWarps ? best_slot[lane] : -1;
+#pragma unroll
+        for (int o = kPaWarps / 2; o > 0; o >>= 1) {
+          const uint64_t k2 = __shfl_xor_sync(0xffffffffu, key, o);
+          const int a2 = __shfl_xor_sync(0xffffffffu, at, o);
+          if (k2 < key || (k2 == key && a2 < at)) key = k2, at = a2;
+        }
+        if (lane == 0) best_key[kPaWarps] = key, best_slot[kPaWarps] = at;
       }
-      cluster.sync();
-      key = kStays;
-      slot = -1;
-      for (int q = 0; q < ctas; ++q) {
-        const uint64_t k2 = *cluster.map_shared_rank(&best_key[kPaWarps], q);
-        const int a2 = *cluster.map_shared_rank(&best_slot[kPaWarps], q);
-        if (k2 < key || (k2 == key && a2 < slot)) key = k2, slot = a2;
+      if (ctas > 1) {
+        cluster.sync();
+        if (cta == 0 && warp == 0) {
+          key = kStays;
+          at = -1;
+          if (lane < ctas) {
+            key = *cluster.map_shared_rank(&best_key[kPaWarps], lane);
+            at = *cluster.map_shared_rank(&best_slot[kPaWarps], lane);
+          }
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) {
+            const uint64_t k2 = __shfl_xor_sync(0xffffffffu, key, o);
+            const int a2 = __shfl_xor_sync(0xffffffffu, at, o);
+            if (k2 < key || (k2 == key && a2 < at)) key = k2, at = a2;
+          }
+        }
       }
+      slot = key == kStays ? -1 : at;
+      old = 0x7fffffff - static_cast<int>(static_cast<uint32_t>(key));
     }
-    cluster.sync();                                      // count and minima are read
+    // Thread 0 has the slot; every CTA's count and minimum has been read.
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
     if (cta != 0) return;
     if (tid == 0) {
-      place(0, 0, slot);
+      one = place(0, slot, old);
       p.c.count[row] = min(n + 1, cap);
       p.c.seen[row] = seen + 1;
     }
-    __syncthreads();
-    copy(1);
+    if (warp == 0) {
+      __syncwarp();
+      copy_rows<D, kF8, 32, 1>(p.c, k_src, v_src, p.token_stride, h, &one, 1);
+    }
   } else {
-    // Tokens for free slots, dealt to the cluster's CTAs in runs of kPaThreads.
-    for (int base = cta * kPaThreads; base < f; base += ctas * kPaThreads) {
-      const int k = min(kPaThreads, f - base);
-      if (tid < k) place(tid, base + tid, n + base + tid);
-      __syncthreads();
-      copy(k);
-      __syncthreads();
+    // Rows to write, up to kPaList at a time, where the histograms are at other times.
+    RowEntry* list = reinterpret_cast<RowEntry*>(hist);
+    const uint32_t lanes_below = (1u << lane) - 1u;
+    // Tokens for free slots: an even share for each CTA of the cluster.
+    if (f > 0) {
+      const int share = (f + ctas - 1) / ctas, f0 = min(f, cta * share), f1 = min(f, f0 + share);
+      for (int done = f0; done < f1; done += kPaList) {
+        const int entries = min(f1 - done, kPaList);
+        for (int i = tid; i < entries; i += kPaThreads) list[i] = place(done + i, n + done + i, -1);
+        __syncthreads();
+        copy_rows<D, kF8, kPaThreads, 8>(p.c, k_src, v_src, p.token_stride, h, list, entries);
+        __syncthreads();
+      }
     }
     if (e > 0) {
       for_keys([&](int s, uint64_t k) { keys[s - s0] = k; });
-      __syncthreads();
       // Radix select, smallest first.  A key with (key & mask) < prefix is taken, one with == prefix is undecided.
+      // Each pass also finds which bits vary among the undecided keys, so that the next digit starts at the first one
+      // that does: weights that are all equal cost one pass, not three, before positions decide.
       uint64_t prefix = 0, mask = 0;
       uint32_t need = static_cast<uint32_t>(e);          // still to take among the undecided
       bool whole = false;                                // every undecided key is taken
-      int pass = 0;
-      for (int shift = 56; shift >= 0; shift -= 8, ++pass) {
+      int top = 64;                                      // bits top .. 63 are decided
+      for (int pass = 0; top > 0; ++pass) {
+        const int bits = min(top, kPaBits), shift = top - bits;
         uint32_t* mine = hist[pass & 1];
-        mine[tid] = 0;
+        for (int i = tid; i < kPaBins / 4; i += kPaThreads) reinterpret_cast<uint4*>(mine)[i] = make_uint4(0, 0, 0, 0);
+        if (tid == 0) sel[2] = 0;
+        if (tid < 4) vary[pass & 1][tid] = tid < 2 ? ~0u : 0u;
         __syncthreads();
-        for (int i = tid; i < s1 - s0; i += kPaThreads) {
-          const uint64_t k = keys[i];
-          if (k != kStays && (k & mask) == prefix) atomicAdd(&mine[(k >> shift) & 255u], 1u);
+        uint64_t every = ~0ull, any = 0;                 // AND and OR of the undecided keys
+        for (int base = 0; base < s1 - s0; base += kPaThreads) {
+          const int i = base + tid;
+          const uint64_t k = i < s1 - s0 ? keys[i] : kStays;
+          const bool in = k != kStays && (k & mask) == prefix;
+          const uint32_t digit = static_cast<uint32_t>(k >> shift) & ((1u << bits) - 1);
+          const uint32_t votes = __ballot_sync(0xffffffffu, in);
+          if (votes == 0) continue;
+          if (in) every &= k, any |= k;
+          // Counters that many keys share would serialise the lanes: one addition where a warp's keys agree.
+          const int lead = __ffs(votes) - 1;
+          const uint32_t first = __shfl_sync(0xffffffffu, digit, lead);
+          const uint32_t same = __ballot_sync(0xffffffffu, in && digit == first);
+          if (lane == lead) atomicAdd(&mine[first], static_cast<uint32_t>(__popc(same)));
+          if (in && digit != first) atomicAdd(&mine[digit], 1u);
+        }
+        {
+          const uint32_t a1 = __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(every >> 32));
+          const uint32_t a0 = __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(every));
+          const uint32_t o1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32));
+          const uint32_t o0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+          if (lane == 0) {
+            atomicAnd(&vary[pass & 1][0], a1);
+            atomicAnd(&vary[pass & 1][1], a0);
+            atomicOr(&vary[pass & 1][2], o1);
+            atomicOr(&vary[pass & 1][3], o0);
+          }
         }
         cluster.sync();        // a buffer is cleared again two passes on, past a barrier after its last reader
-        uint32_t c = 0;
-        for (int q = 0; q < ctas; ++q) c += cluster.map_shared_rank(mine, q)[tid];
-        uint32_t incl = c;
+        constexpr int kPer = kPaBins / kPaThreads;       // consecutive counters of a thread
+        static_assert(kPer == 4, "one 16-byte word of counters per thread");
+        uint32_t c[kPer] = {}, all = 0;
+#pragma unroll
+        for (int q0 = 0; q0 < 8; q0 += 4) {              // four peers' words on their way at a time
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (q0 + i < ctas) x[i] = reinterpret_cast<const uint4*>(cluster.map_shared_rank(mine, q0 + i))[tid];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[0] += x[i].x, c[1] += x[i].y, c[2] += x[i].z, c[3] += x[i].w;
+        }
+        if (warp == 0) {
+          uint4 v = make_uint4(~0u, ~0u, 0u, 0u);
+          if (lane < ctas) v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(vary[pass & 1], lane));
+          v.x = __reduce_and_sync(0xffffffffu, v.x), v.y = __reduce_and_sync(0xffffffffu, v.y);
+          v.z = __reduce_or_sync(0xffffffffu, v.z), v.w = __reduce_or_sync(0xffffffffu, v.w);
+          if (lane == 0) every_any[0] = (static_cast<uint64_t>(v.x) << 32) | v.y, every_any[1] = (static_cast<uint64_t>(v.z) << 32) | v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) all += c[i];
+        uint32_t incl = all;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += y;
         }
         if (lane == 31) warp_sum[warp] = incl;
-        if (tid == 0) sel[2] = 0;
         __syncthreads();
         for (int w = 0; w < warp; ++w) incl += warp_sum[w];
-        if (incl >= need && incl - c < need) {           // the digit that holds the need-th key
-          sel[0] = tid;
-          sel[1] = need - (incl - c);
-          sel[2] = c == need - (incl - c) ? 2 : 1;
+        if (incl >= need && incl - all < need) {         // this thread's counters hold the need-th key
+          uint32_t before = incl - all, digit = 0, size = 0;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (size == 0) {
+              if (before + c[i] >= need) digit = tid * kPer + i, size = c[i];
+              else before += c[i];
+            }
+          sel[0] = digit;
+          sel[1] = need - before;
+          sel[2] = size == need - before ? 2 : 1;
         }
         __syncthreads();
         const uint32_t state = sel[2];
@@ -220,77 +307,112 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const __grid_c
           break;
         }
         prefix |= static_cast<uint64_t>(sel[0]) << shift;
-        mask |= 255ull << shift;
+        mask |= ((uint64_t(1) << bits) - 1) << shift;
         need = sel[1];
-        __syncthreads();
         if (state == 2) {
           whole = true;
           break;
         }
+        // The undecided keys agree in every bit from `shift` up now; of those below, skip the ones in which not even
+        // this pass's keys differed.
+        every = every_any[0];
+        const uint64_t below = shift == 0 ? 0 : (every ^ every_any[1]) & ((uint64_t(1) << shift) - 1);
+        const int next = below == 0 ? 0 : 64 - __clzll(static_cast<long long>(below));
+        const uint64_t agreed = shift == 0 ? 0 : ((uint64_t(1) << shift) - 1) & ~((uint64_t(1) << next) - 1);
+        prefix |= every & agreed;
+        mask |= agreed;
+        top = next;
+        __syncthreads();                                 // the shared words of this pass are read
       }
       // Victims of this slice: those below the prefix, and of the undecided all or (equal keys, which need equal
-      // positions) the first `need` in slot order.
-      uint32_t below = 0, equal = 0;
-      for (int i = tid; i < s1 - s0; i += kPaThreads) {
-        const uint64_t k = keys[i];
-        if (k == kStays) continue;
-        below += (k & mask) < prefix || (whole && (k & mask) == prefix);
-        equal += !whole && (k & mask) == prefix;
+      // positions) the first `need` in slot order.  A warp looks at `per` steps of 32 consecutive slots, so that
+      // slot order is warp, step, lane; a thread remembers what it saw in a bit per step.
+      const int per = (p.slice + kPaThreads - 1) / kPaThreads;         // <= 32
+      const int i0 = warp * per * 32 + lane;
+      uint32_t below_bits = 0, equal_bits = 0;
+      for (int j = 0; j < per; ++j) {
+        const int i = i0 + 32 * j;
+        const uint64_t k = i < s1 - s0 ? keys[i] : kStays;
+        const uint64_t head = k & mask;
+        below_bits |= static_cast<uint32_t>(k != kStays && (head < prefix || (whole && head == prefix))) << j;
+        equal_bits |= static_cast<uint32_t>(k != kStays && !whole && head == prefix) << j;
       }
-      uint32_t both = below | (equal << 16);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
-      if (lane == 0) warp_sum[warp] = both;
+      // Exclusive scan over the warps, and the totals for the cluster.
+      const uint32_t below_w = __reduce_add_sync(0xffffffffu, __popc(below_bits));
+      const uint32_t equal_w = __reduce_add_sync(0xffffffffu, __popc(equal_bits));
+      if (lane == 0) warp_sum[warp] = below_w | (equal_w << 16);       // at most 1,024 each
       __syncthreads();
-      if (tid == 0) {
-        uint32_t all = 0;
-        for (int w = 0; w < kPaWarps; ++w) all += warp_sum[w];
-        taken_here = all;
+      uint32_t below = 0, equal = 0, below_all = 0, equal_all = 0;
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) {
+        const uint32_t x = warp_sum[w];
+        below_all += x & 0xffffu, equal_all += x >> 16;
+        if (w < warp) below += x & 0xffffu, equal += x >> 16;
       }
+      if (tid == 0) taken_here[0] = below_all, taken_here[1] = equal_all;
       cluster.sync();
-      uint32_t rank = 0, all_taken = 0, seen_equal = 0, eq_all_before = 0;   // victims and undecided before this slice
-      for (int q = 0; q < ctas; ++q) {
-        const uint32_t x = *cluster.map_shared_rank(&taken_here, q);
-        const uint32_t eq = x >> 16, left = need > eq_all_before ? need - eq_all_before : 0u;
-        const uint32_t take = (x & 0xffffu) + min(eq, left);
-        if (q == cta) seen_equal = eq_all_before;
-        if (q < cta) rank += take;
-        all_taken += take;
-        eq_all_before += eq;
+      if (warp == 0) {
+        // Lane q holds slice q's counts; undecided keys are taken in slice order until `need` are.
+        uint32_t bel = 0, eq = 0;
+        if (lane < ctas) {
+          const uint32_t* x = cluster.map_shared_rank(taken_here, lane);
+          bel = x[0], eq = x[1];
+        }
+        uint32_t eq_incl = eq;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, eq_incl, o);
+          if (lane >= o) eq_incl += y;
+        }
+        const uint32_t eq_excl = eq_incl - eq;
+        const uint32_t take = bel + min(eq, need > eq_excl ? need - eq_excl : 0u);
+        uint32_t incl = take;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == cta) ranks[0] = incl - take, ranks[2] = eq_excl;
+        if (lane == 7) ranks[1] = incl;
       }
-      for (int base = s0; base < s1; base += kPaThreads) {
-        const int s = base + tid;
-        const uint64_t k = s < s1 ? keys[s - s0] : kStays;
-        const bool eq = k != kStays && (k & mask) == prefix;
-        const uint32_t eq_bits = __ballot_sync(0xffffffffu, eq && !whole);
-        if (lane == 0) warp_sum[warp] = __popc(eq_bits);
-        __syncthreads();
-        uint32_t eq_rank = seen_equal + __popc(eq_bits & ((1u << lane) - 1u));
-        uint32_t eq_all = 0;
-        for (int w = 0; w < kPaWarps; ++w) {
-          eq_rank += w < warp ? warp_sum[w] : 0u;
-          eq_all += warp_sum[w];
+      __syncthreads();
+      const uint32_t rank0 = ranks[0], all_taken = ranks[1], seen_equal = ranks[2];
+      const uint32_t left = need > seen_equal ? need - seen_equal : 0u;     // undecided ones that this slice gives
+      uint32_t goes = below_bits;
+      if (!whole) {
+        uint32_t eq_rank = equal;
+        for (int j = 0; j < per; ++j) {
+          const uint32_t votes = __ballot_sync(0xffffffffu, (equal_bits >> j) & 1u);
+          if (((equal_bits >> j) & 1u) && eq_rank + __popc(votes & lanes_below) < left) goes |= 1u << j;
+          eq_rank += __popc(votes);
         }
-        const bool goes = k != kStays && ((k & mask) < prefix || (eq && (whole || eq_rank < need)));
-        const uint32_t bits = __ballot_sync(0xffffffffu, goes);
-        __syncthreads();
-        if (lane == 0) warp_sum[warp] = __popc(bits);
-        __syncthreads();
-        uint32_t at = __popc(bits & ((1u << lane) - 1u)), all = 0;
-        for (int w = 0; w < kPaWarps; ++w) {
-          at += w < warp ? warp_sum[w] : 0u;
-          all += warp_sum[w];
+      }
+      const int here = static_cast<int>(below_all + min(equal_all, left));
+      const uint32_t first = below + min(equal, left);                      // rank of this warp's first victim
+      for (int done = 0; done < here; done += kPaList) {
+        // Slots and positions in slot order, then a row entry for each.
+        uint32_t rank = first - static_cast<uint32_t>(done);                // wraps: outside the list
+        for (int j = 0; j < per; ++j) {
+          const bool go = (goes >> j) & 1u;
+          const uint32_t votes = __ballot_sync(0xffffffffu, go);
+          const uint32_t at = rank + __popc(votes & lanes_below);
+          if (go && at < kPaList) {
+            const int i = i0 + 32 * j;
+            list[at] = {s0 + i, 0x7fffffffu - static_cast<uint32_t>(keys[i])};
+          }
+          rank += __popc(votes);
         }
-        if (goes) place(at, f + rank + at, s);
         __syncthreads();
-        copy(all);
+        const int entries = min(here - done, kPaList);
+        for (int i = tid; i < entries; i += kPaThreads)
+          list[i] = place(f + static_cast<int>(rank0) + done + i, list[i].page, static_cast<int>(list[i].off_tok));
         __syncthreads();
-        rank += all;
-        seen_equal += eq_all;
+        copy_rows<D, kF8, kPaThreads, 8>(p.c, k_src, v_src, p.token_stride, h, list, entries);
+        __syncthreads();
       }
       // Tokens for which no slot may be replaced.
       if (cta == 0)
-        for (int i = f + all_taken + tid; i < m; i += kPaThreads) place(tid, i, -1);
+        for (int i = f + static_cast<int>(all_taken) + tid; i < m; i += kPaThreads) place(i, -1, -2);
     }
     cluster.sync();                                      // the cluster has read counts, histograms and sums
     if (cta == 0 && tid == 0) {
@@ -300,17 +422,25 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const __grid_c
   }
 }
 
-// CTAs per row: the largest of 8, 4, 2, 1 whose clusters leave two CTAs per
-// SM at most and 1,024 slots per CTA at least, but enough for the slice to fit.
+// CTAs per row.  One out: the largest of 8, 4, 2, 1 whose clusters leave two
+// CTAs per SM at most and 1,024 slots per CTA at least.  Several out: the
+// fewest that leave slices of 8,192 slots at most, and more while the CTAs do
+// not fill the SMs and slices are over 2,048 slots: every pass of the select
+// is a barrier of the cluster (24 x 8 rows of 16,000 slots: AC8 us with 8
+// CTAs of 256 threads per row, AC2 us with 2 of 512).
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
-  int ctas = 8;
-  while (ctas > 1 && (rows * ctas > 2 * 148 || p.c.capacity < 1024 * ctas)) ctas >>= 1;
-  while (ctas < 8 && (p.c.capacity + ctas - 1) / ctas > kPaMaxSlice) ctas <<= 1;
-  p.slice = ((p.c.capacity + ctas - 1) / ctas + 7) / 8 * 8;
   const bool chunk = !p.one_each;
+  int ctas = 1;
+  if (chunk) {
+    while (ctas < 8 && (p.c.capacity > 8192 * ctas || (rows * ctas < 148 && p.c.capacity > 2048 * ctas))) ctas <<= 1;
+  } else {
+    ctas = 8;
+    while (ctas > 1 && (rows * ctas > 2 * 148 || p.c.capacity < 1024 * ctas)) ctas >>= 1;
+  }
+  p.slice = ((p.c.capacity + ctas - 1) / ctas + 7) / 8 * 8;
   const size_t smem = chunk ? static_cast<size_t>(p.slice) * 8 : 0;
-  const dim3 grid(static_cast<unsigned>(rows * ctas)), block(kPaThreads);
+  const dim3 grid(static_cast<unsigned>(rows * ctas)), block(append_threads(chunk));
   static std::atomic<uint64_t> ready[4];
   auto go = [&](auto kern, int which) {
     if (smem > 0) {

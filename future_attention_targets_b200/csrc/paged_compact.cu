@@ -39,9 +39,9 @@ __device__ __forceinline__ int block_sum_scan(int x, int* sums, int* total) {
 }
 
 template <int D, bool kF8>
-__global__ void __launch_bounds__(kPcThreads) paged_compact_kernel(const __grid_constant__ PagedCompactParams p) {
+__global__ void __launch_bounds__(kPcThreads, 4) paged_compact_kernel(const __grid_constant__ PagedCompactParams p) {
   __shared__ int sums[kPcWarps];
-  __shared__ int32_t l_page[kPcMaxBlock], l_off[kPcMaxBlock], l_tok[kPcMaxBlock];
+  __shared__ RowEntry list[kPcMaxBlock];
   const int tid = threadIdx.x;
   const int row = blockIdx.x, b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
   const int s0 = p.start[b], L = p.start[b + 1] - s0;
@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kPcThreads) paged_compact_kernel(const __grid_
     const uint4* v = reinterpret_cast<const uint4*>(mask + head);
     // Non-zero bytes: bit 7 of ((x & 0x7f) + 0x7f) | x, which cannot carry into the next byte.
     auto bits = [](uint32_t x) { return __popc((((x & 0x7f7f7f7fu) + 0x7f7f7f7fu) | x) & 0x80808080u); };
+#pragma unroll 4
     for (int i = tid; i < words; i += kPcThreads) {
       const uint4 x = __ldg(v + i);
       c += bits(x.x) + bits(x.y) + bits(x.z) + bits(x.w);
@@ -83,9 +84,7 @@ __global__ void __launch_bounds__(kPcThreads) paged_compact_kernel(const __grid_
     if (rank < n) {
       const int slot = before + rank, off = slot & ((1 << p.c.page_shift) - 1);
       const int page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_COMPACT, 1);
-      l_page[rank] = page;
-      l_off[rank] = off;
-      l_tok[rank] = s0 + first + i;
+      list[rank] = row_entry(page, off, first + i);
       if (page >= 0) {
         const int64_t at = ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) + off;
         if (p.c.pos != nullptr) p.c.pos[at] = first + i;
@@ -100,13 +99,16 @@ __global__ void __launch_bounds__(kPcThreads) paged_compact_kernel(const __grid_
     if (p.c.seen != nullptr) p.c.seen[row] = L;
   }
   __syncthreads();
-  copy_rows<D, kF8, kPcThreads, 8>(p.c, p.k, p.v, static_cast<int64_t>(p.c.n_kv_heads) * D, h, {l_page, l_off, l_tok}, n);
+  const int64_t stride = static_cast<int64_t>(p.c.n_kv_heads) * D;
+  copy_rows<D, kF8, kPcThreads, kF8 ? 4 : 8>(p.c, p.k + s0 * stride, p.v + s0 * stride, stride, h, list, n);
 }
 
 cudaError_t launch_paged_compact(PagedCompactParams& p, int head_dim, bool f8, cudaStream_t stream) {
   int longest = 1;
   for (int b = 0; b < p.c.batch; ++b) longest = std::max(longest, p.start[b + 1] - p.start[b]);
-  p.block = kPcMaxBlock;
+  // 256 positions per CTA keep the CTAs many and even (8 prompts of 100,003 tokens in all: PK256 us, with 1,024 PK1024);
+  // beyond 32,768 tokens counting the mask again 4 times as often would show.
+  p.block = longest <= 32768 ? 256 : kPcMaxBlock;
   const dim3 grid(p.c.batch * p.c.n_kv_heads, (longest + p.block - 1) / p.block), block(kPcThreads);
   if (head_dim == 128)
     return f8 ? launch_paged(paged_compact_kernel<128, true>, grid, block, 0, 1, stream, p)

@@ -52,7 +52,7 @@ typedef enum {
 typedef struct {
   void* k_pages;              /* 16-byte aligned, as are all strides in bytes */
   void* v_pages;
-  int64_t k_stride[3];        /* elements between pages, heads, slots; >= 0 */
+  int64_t k_stride[3];        /* elements between pages, heads, slots; >= 0, pages and slots below 4 GiB */
   int64_t v_stride[3];
   int32_t* pos_pages;         /* [n_pages, n_kv_heads, page_size]: position of the token in a slot; 16-byte aligned */
   float* weight_pages;        /* the same layout: attention weight it has accumulated; 16-byte aligned */
@@ -96,7 +96,7 @@ KVPOP_API kvpop_status kvpop_paged_compact_kv(const void* k, const void* v, cons
  * the remaining new tokens in theirs.  A new token's position is seen + its
  * place among the m_b, its weight 0.  count and seen are advanced.
  *   k_new, v_new   bf16 [T_new, n_kv_heads, head_dim], token_stride elements between tokens
- *                  (a multiple of 8; head_dim and heads contiguous), 16-byte aligned
+ *                  (a multiple of 8, below 4 GiB; head_dim and heads contiguous), 16-byte aligned
  *   cu_new         HOST int32 [batch + 1], offsets of each sequence's new tokens; NULL = one token each
  *   window, sinks  every m_b <= max(window, 1); capacity >= sinks + max(window, 1)
  *   evicted        int32 [T_new, n_kv_heads] or NULL: the position that a token displaced, -1 where it took a

@@ -226,6 +226,18 @@ def test_compact_rounds_and_clips_to_e4m3():
     ref.assert_same_state(a, want)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.7, 0.02, 3e-3, 2.0 ** -20, 1e-39, 2e38, 117.3])
+def test_compact_every_bf16_value_to_e4m3(scale):
+    """All 65,536 bf16 bit patterns over several scales: the rounding of the correctly rounded quotient, bit for bit."""
+    k = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(1024, 1, 64)
+    a = ref.make_cache(1, 1, 64, 64, 1024, "e4m3")
+    a["k_scale"].fill_(scale)
+    a["v_scale"].fill_(scale * 1.7)
+    want = ref.compact(a, k, k, None, [0, 1024], None)
+    kv.paged_compact_kv(k.cuda(), k.cuda(), None, [0, 1024], kv.PagedCache(**a))
+    ref.assert_same_state(a, want)
+
+
 def test_compact_bad_page_is_left_out():
     a = ref.make_cache(1, 1, 64, 8, 64, seed=2)
     k = torch.randn(64, 1, 64, generator=gen(1)).to(torch.bfloat16)
