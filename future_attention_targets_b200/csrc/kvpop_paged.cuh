@@ -98,13 +98,18 @@ __device__ __forceinline__ RowEntry row_entry(int page, int off, int tok) {
   return {page, static_cast<uint32_t>(off) | (static_cast<uint32_t>(tok) << 10)};
 }
 
-// Products of two pairs of fp32 values, each rounded once.
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 __device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) { return (static_cast<uint64_t>(hi) << 32) | lo; }
+__device__ __forceinline__ uint64_t twice(float x) { return pair_of(__float_as_uint(x), __float_as_uint(x)); }
 // Two fp32 values to two e4m3, nearest even, clipped to +-448; NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(uint64_t x) {
   uint16_t r;
@@ -114,35 +119,47 @@ __device__ __forceinline__ uint32_t e4m3x2(uint64_t x) {
   return r;
 }
 
-// What a cache row's values are divided by.  Rounding to e4m3 is monotonic, so where x * low and x * high, which
-// enclose the quotient, round to the same value, the correctly rounded fp32 quotient does too; else the kernel
-// divides.  low and high are the reciprocal 2^-21 to either side (it is off by 2^-24 itself and the products by as
-// much), or the reciprocal itself for a power of two, whose quotients are exact.  A division for every element
-// bound an 8-bit cache's compaction (8 prompts, 100,003 tokens: 127 us).
+// What the rows of an 8-bit cache are divided by, and the division: the correctly rounded fp32 quotient, two at a
+// time.  x is clipped to just past +-464 scale, beyond which everything rounds to +-448, so that nothing overflows;
+// the product of -x with the negated rounded reciprocal is then corrected by its exact remainder (P. Markstein, IBM
+// J. Res. Dev. 34(1), 1990), with signs that keep -0.  That is correctly rounded wherever the remainder does not
+// underflow, which for scales of 2^-60 to 2^60 is every quotient that e4m3 does not flush to 0.  Other scales divide.
+// With a division for every element an 8-bit cache's compaction was bound by it (8 prompts, 100,003 tokens: 127 us),
+// with two conversions to enclose the quotient by those (104 us).
 struct Divisor {
   float scale;
-  uint64_t low, high;     // twice each
+  bool divide;
+  uint32_t clip, clip_neg;       // bf16x2
+  uint64_t neg_inv, scale2;
 };
 __device__ __forceinline__ Divisor divisor_of(float scale) {
-  const float inv = __frcp_rn(scale);
-  const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0u && inv >= 0x1p-126f && inv <= 0x1p126f;
-  // A reciprocal out of the normal range says nothing: enclose everything.
-  const bool odd = !(inv >= 0x1p-100f && inv <= 0x1p100f);
-  const float lo = exact ? inv : odd ? 0.f : __fmul_rn(inv, 1.f - 0x1p-21f);
-  const float hi = exact ? inv : odd ? INFINITY : __fmul_rn(inv, 1.f + 0x1p-21f);
-  const uint32_t l = __float_as_uint(lo), h = __float_as_uint(hi);
-  return {scale, pair_of(l, l), pair_of(h, h)};
+  Divisor d;
+  d.scale = scale;
+  d.divide = !(scale >= 0x1p-60f && scale <= 0x1p60f);
+  d.clip = (__float_as_uint(500.f * scale) >> 16) * 0x10001u;      // bf16, rounded down: at least 496 scale
+  d.clip_neg = d.clip | 0x80008000u;
+  d.neg_inv = twice(-__frcp_rn(scale));
+  d.scale2 = twice(scale);
+  return d;
 }
 __device__ __forceinline__ uint2 to_e4m3x8(const uint4& in, const Divisor& by) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
   uint32_t r[4];
+  if (by.divide) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint64_t x = pair_of(w[e] << 16, w[e] & 0xffff0000u);
-    r[e] = e4m3x2(mul2(x, by.low));
-    if (r[e] != e4m3x2(mul2(x, by.high)))
+    for (int e = 0; e < 4; ++e)
       r[e] = e4m3x2(pair_of(__float_as_uint(__fdiv_rn(__uint_as_float(w[e] << 16), by.scale)),
                             __float_as_uint(__fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), by.scale))));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t y = w[e] ^ 0x80008000u;
+      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(by.clip));
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(by.clip_neg));
+      const uint64_t neg_x = pair_of(y << 16, y & 0xffff0000u);
+      const uint64_t q = mul2(neg_x, by.neg_inv);
+      r[e] = e4m3x2(fma2(fma2(q, by.scale2, neg_x), by.neg_inv, q));
+    }
   }
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }

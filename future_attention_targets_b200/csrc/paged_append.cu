@@ -30,12 +30,25 @@ constexpr int kPaBins = 1 << kPaBits;
 constexpr int kPaList = 2 * kPaBins * 4 / static_cast<int>(sizeof(RowEntry));   // as the two histograms
 constexpr uint64_t kStays = ~0ull;
 
-// Larger float -> larger key; -0 equals +0 (the addition makes it +0); NaN -> 0, below every number.
+// Larger float -> larger key, never 2^32 - 1; -0 equals +0 (the addition makes it +0); NaN -> 0, below every number
+// (the addition's NaN is the canonical 0x7fffffff, whose key 2^32 - 1 wraps to 0 with the one added to all).
 __device__ __forceinline__ uint32_t weight_key(float f) {
-  f = __fadd_rn(f, 0.f);
-  const uint32_t u = __float_as_uint(f);
-  const uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
-  return f != f ? 0u : key;
+  const uint32_t u = __float_as_uint(__fadd_rn(f, 0.f));
+  return (u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u)) + 1u;
+}
+
+// The one of a warp's candidates that goes first: least key, then largest position, then smallest slot (at < 0: no
+// candidate, with key ~0).  Every lane gets it.
+struct Candidate {
+  uint32_t key;
+  int pos, at;
+};
+__device__ __forceinline__ Candidate first_to_go(const Candidate& c) {
+  Candidate r;
+  r.key = __reduce_min_sync(0xffffffffu, c.key);
+  r.pos = __reduce_max_sync(0xffffffffu, c.key == r.key ? c.pos : -1);
+  r.at = static_cast<int>(__reduce_min_sync(0xffffffffu, c.key == r.key && c.pos == r.pos ? static_cast<uint32_t>(c.at) : ~0u));
+  return r;
 }
 
 template <int D, bool kF8, bool kChunk>
@@ -45,8 +58,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   cg::cluster_group cluster = cg::this_cluster();
   const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
   extern __shared__ __align__(16) uint64_t keys[];       // kChunk: this CTA's slice; then the rows to write
-  __shared__ uint64_t best_key[kPaWarps + 1];            // one out: minimum of each warp; [kPaWarps] = of the CTA
-  __shared__ int32_t best_slot[kPaWarps + 1];
+  __shared__ Candidate best[kPaWarps + 1];               // one out: of each warp; [kPaWarps] = of the CTA
   __shared__ __align__(16) uint32_t hist[kChunk ? 2 : 1][kChunk ? kPaBins : 4];   // a pass's histogram, read by the cluster
   __shared__ __align__(16) uint32_t vary[2][4];          // AND and OR of a pass's keys, high and low halves
   __shared__ uint64_t every_any[2];                      // the same of the whole cluster
@@ -54,7 +66,6 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   __shared__ uint32_t ranks[3];                          // victims before this slice, victims in all, undecided before it
   __shared__ uint32_t taken_here[2];                     // kChunk: victims and undecided in this slice, read by the cluster
   __shared__ uint32_t warp_sum[kPaWarps];
-  __shared__ RowEntry one;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / ctas, b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
@@ -64,6 +75,23 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   if (m == 0) return;                                    // as for every branch on b or count: the whole cluster
   grid_wait();
   grid_launch_next();
+  // One out: a thread's slots are four at a time, kU times; their page numbers, and the new rows (a 16-byte word per
+  // lane of warp 0), are on their way together with the row's counts.
+  constexpr int kU = 4;
+  const int s_lo = cta * p.slice;
+  int raw[kU];
+  uint4 fresh = make_uint4(0, 0, 0, 0);
+  if constexpr (!kChunk) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int s = s_lo + 4 * (tid + u * kPaThreads);
+      raw[u] = s < min(s_lo + p.slice, p.c.capacity) ? p.c.table[static_cast<int64_t>(b) * p.c.max_pages + (s >> p.c.page_shift)] : -1;
+    }
+    if (cta == 0 && tid < D / 4) {
+      const uint16_t* from = (tid < D / 8 ? p.k_new : p.v_new) + tok0 * p.token_stride + static_cast<int64_t>(h) * D + 8 * (tid % (D / 8));
+      fresh = __ldg(reinterpret_cast<const uint4*>(from));
+    }
+  }
   const int count = p.c.count[row], seen = p.c.seen[row];
   if (count < 0) {
     if (p.evicted != nullptr && cta == 0)
@@ -82,14 +110,13 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
     return ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) + off;
   };
   auto key_of = [&](float w, int pos) {
-    // pos < 0 wraps to a large number that no span reaches.
-    const bool goes = pos >= 0 && static_cast<uint32_t>(pos) - static_cast<uint32_t>(p.sinks) < span && pos >= p.sinks;
+    // Positions below sinks wrap to numbers from 2^31 - sinks up, which no span exceeds.
+    const bool goes = static_cast<uint32_t>(pos) - static_cast<uint32_t>(p.sinks) < span;
     return goes ? (static_cast<uint64_t>(weight_key(w)) << 32) | static_cast<uint32_t>(0x7fffffff - pos) : kStays;
   };
   // Calls use(slot, keys) for the slots of this CTA's slice, 4 per thread and step (a page has at least 8 slots and
   // slices are multiples of 8, so four slots share a page and an aligned 16 bytes).
   auto for_keys = [&](auto&& use) {
-    constexpr int kU = 4;
     for (int base = s0 + 4 * tid; base < s1; base += 4 * kPaThreads * kU) {
       int page[kU];
       float4 w[kU];
@@ -139,62 +166,98 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   if constexpr (!kChunk) {
     int slot = n, old = -1;                              // the free slot, if there is one
     if (e > 0) {
-      uint64_t key = kStays;
-      int at = -1;
-      for_keys([&](int s, uint64_t k) {
-        if (k < key) key = k, at = s;
-      });
+      Candidate c = {~0u, -1, -1};
+      for (int base = s_lo + 4 * tid; base < s1; base += 4 * kPaThreads * kU) {
+        float4 w[kU];
+        int4 x[kU];
+        if (base != s_lo + 4 * tid)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t k2 = __shfl_xor_sync(0xffffffffu, key, o);
-        const int a2 = __shfl_xor_sync(0xffffffffu, at, o);
-        if (k2 < key || (k2 == key && a2 < at)) key = k2, at = a2;
+          for (int u = 0; u < kU; ++u) {
+            const int s = base + u * 4 * kPaThreads;
+            raw[u] = s < s1 ? p.c.table[static_cast<int64_t>(b) * p.c.max_pages + (s >> p.c.page_shift)] : -1;
+          }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int s = base + u * 4 * kPaThreads;
+          x[u] = make_int4(-1, -1, -1, -1);              // a position that never goes
+          w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (s < s1) {
+            if (static_cast<uint32_t>(raw[u]) < static_cast<uint32_t>(p.c.n_pages)) {
+              const int64_t from = meta_at(raw[u], s & page_mask);
+              w[u] = *reinterpret_cast<const float4*>(p.c.weight + from);
+              x[u] = *reinterpret_cast<const int4*>(p.c.pos + from);
+              if (s + 3 >= s1) {
+                x[u].w = -1;
+                if (s + 2 >= s1) x[u].z = -1;
+                if (s + 1 >= s1) x[u].y = -1;
+              }
+            } else {
+              debug_fail(p.status, DBG_PAGED_APPEND, 1);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const float wf[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+          const int xi[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool goes = static_cast<uint32_t>(xi[i]) - static_cast<uint32_t>(p.sinks) < span;
+            const uint32_t k = goes ? weight_key(wf[i]) : ~0u;
+            const bool better = (k < c.key) | ((k == c.key) & (xi[i] > c.pos) & goes);
+            c.key = better ? k : c.key;
+            c.pos = better ? xi[i] : c.pos;
+            c.at = better ? base + u * 4 * kPaThreads + i : c.at;
+          }
+        }
       }
-      if (lane == 0) best_key[warp] = key, best_slot[warp] = at;
+      c = first_to_go(c);
+      if (lane == 0) best[warp] = c;
       __syncthreads();
       if (warp == 0) {
-        key = lane < kPaWarps ? best_key[lane] : kStays;
-        at = lane < kPaWarps ? best_slot[lane] : -1;
-#pragma unroll
-        for (int o = kPaWarps / 2; o > 0; o >>= 1) {
-          const uint64_t k2 = __shfl_xor_sync(0xffffffffu, key, o);
-          const int a2 = __shfl_xor_sync(0xffffffffu, at, o);
-          if (k2 < key || (k2 == key && a2 < at)) key = k2, at = a2;
-        }
-        if (lane == 0) best_key[kPaWarps] = key, best_slot[kPaWarps] = at;
+        c = lane < kPaWarps ? best[lane] : Candidate{~0u, -1, -1};
+        c = first_to_go(c);
+        if (lane == 0) best[kPaWarps] = c;
       }
       if (ctas > 1) {
         cluster.sync();
         if (cta == 0 && warp == 0) {
-          key = kStays;
-          at = -1;
-          if (lane < ctas) {
-            key = *cluster.map_shared_rank(&best_key[kPaWarps], lane);
-            at = *cluster.map_shared_rank(&best_slot[kPaWarps], lane);
-          }
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) {
-            const uint64_t k2 = __shfl_xor_sync(0xffffffffu, key, o);
-            const int a2 = __shfl_xor_sync(0xffffffffu, at, o);
-            if (k2 < key || (k2 == key && a2 < at)) key = k2, at = a2;
-          }
+          c = lane < ctas ? *cluster.map_shared_rank(&best[kPaWarps], lane) : Candidate{~0u, -1, -1};
+          c = first_to_go(c);
         }
       }
-      slot = key == kStays ? -1 : at;
-      old = 0x7fffffff - static_cast<int>(static_cast<uint32_t>(key));
+      slot = c.key == ~0u ? -1 : c.at;
+      old = c.pos;
     }
-    // Thread 0 has the slot; every CTA's count and minimum has been read.
+    // Warp 0 of CTA 0 has the slot; every CTA's count and candidate has been read.
     if (ctas > 1) cluster.sync();
     else __syncthreads();
     if (cta != 0) return;
-    if (tid == 0) {
-      one = place(0, slot, old);
+    if (warp > 0) return;
+    int page = -1;
+    const int off = slot & page_mask;
+    if (slot >= 0) page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 2);
+    else debug_fail(p.status, DBG_PAGED_APPEND, 3);
+    if (lane == 0) {
       p.c.count[row] = min(n + 1, cap);
       p.c.seen[row] = seen + 1;
+      if (p.evicted != nullptr) p.evicted[static_cast<int64_t>(tok0) * p.c.n_kv_heads + h] = page >= 0 ? old : -2;
+      if (page >= 0) {
+        p.c.pos[meta_at(page, off)] = seen;
+        p.c.weight[meta_at(page, off)] = 0.f;
+      }
     }
-    if (warp == 0) {
-      __syncwarp();
-      copy_rows<D, kF8, 32, 1>(p.c, k_src, v_src, p.token_stride, h, &one, 1);
+    if (page >= 0 && lane < D / 4) {
+      const bool is_v = lane >= D / 8;
+      const int word = lane % (D / 8);
+      uint8_t* to = is_v ? p.c.v + page * p.c.v_page + h * p.c.v_head + off * p.c.v_slot
+                         : p.c.k + page * p.c.k_page + h * p.c.k_head + off * p.c.k_slot;
+      if constexpr (kF8) {
+        const float* scale = is_v ? p.c.v_scale : p.c.k_scale;
+        *reinterpret_cast<uint2*>(to + 8 * word) = to_e4m3x8(fresh, divisor_of(scale != nullptr ? scale[h] : 1.f));
+      } else {
+        *reinterpret_cast<uint4*>(to + 16 * word) = fresh;
+      }
     }
   } else {
     // Rows to write, up to kPaList at a time, where the histograms are at other times.
