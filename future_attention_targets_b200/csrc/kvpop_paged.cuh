@@ -46,8 +46,14 @@ struct PagedDecodeParams {
   float* scores;          // [B * H_q, score_pitch], log2 units; null = weights not accumulated
   int32_t* status;
   int32_t* dbg;
-  int32_t n_q_heads, group, head_chunks, split_slots, n_split, score_pitch;
+  int32_t n_q_heads, group, head_chunks, split_slots, n_split, cluster, score_pitch;   // cluster: a row's splits are one
   float scale_log2;
+};
+
+// How a decode step's rows are cut up.
+struct DecodeSplit {
+  int slots, n;
+  bool cluster;
 };
 
 struct PagedAppendParams {
@@ -210,16 +216,18 @@ __device__ __forceinline__ void copy_rows(const PagedView& c, const uint16_t* k,
   }
 }
 
-// Raises a kernel's dynamic shared memory limit on the current device, once per device (`done`: one bit each).
+// Raises a kernel's dynamic shared memory limit on the current device (and allows clusters of 16), once per device
+// (`done`: one bit each).
 // Another thread may do it again at the same time: that changes nothing.
 template <class Kern>
-static cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<uint64_t>& done) {
+static cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<uint64_t>& done, bool wide_clusters = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && wide_clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }

@@ -18,7 +18,7 @@ namespace kvpop {
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int head_dim, bool f8, cudaStream_t stream);
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream);
 cudaError_t launch_paged_compact(PagedCompactParams& p, int head_dim, bool f8, cudaStream_t stream);
-int paged_split_slots(int64_t rows, int capacity);
+DecodeSplit paged_split(int64_t rows, int capacity, bool may_cluster);
 }  // namespace kvpop
 
 using namespace kvpop;
@@ -36,6 +36,7 @@ constexpr int kMaxCapacity = 131072;
 constexpr int kMaxBatch = 65535;
 constexpr int kMaxKvHeads = 1024;
 constexpr int kMaxQHeads = 1 << 16;
+constexpr int kMaxGroup = 1024;       // query heads per KV head
 
 kvpop_status fail(kvpop_status st, const char* fmt, ...) {
   char buf[512];
@@ -118,7 +119,8 @@ kvpop_status check_offsets(const int32_t* cu, int batch, const char* name) {
 
 // How a decode step is cut up, and where its parts lie in the workspace.
 struct DecodePlan {
-  int head_chunks, split_slots, n_split, score_pitch;
+  int head_chunks, score_pitch;
+  DecodeSplit split;
   size_t ml, o, scores, bytes;
 };
 
@@ -127,13 +129,12 @@ DecodePlan plan_decode(const kvpop_paged_cache& c, int n_q_heads, bool accumulat
   const int group = n_q_heads / c.n_kv_heads;
   d.head_chunks = (group + 15) / 16;
   const int64_t rows = static_cast<int64_t>(c.batch) * c.n_kv_heads * d.head_chunks;
-  d.split_slots = paged_split_slots(rows, c.capacity);
-  d.n_split = (c.capacity + d.split_slots - 1) / d.split_slots;
+  // Heads of several chunks add to the same weights: the second kernel sums those in a fixed order.
+  d.split = paged_split(rows, c.capacity, d.head_chunks == 1 || !accumulate);
   d.score_pitch = (c.capacity + 63) / 64 * 64;
   const size_t heads = static_cast<size_t>(c.batch) * n_q_heads;
-  const bool parts = d.n_split > 1 || accumulate;
-  d.ml = parts ? round256(heads * d.n_split * sizeof(float2)) : 0;
-  d.o = d.n_split > 1 ? round256(heads * d.n_split * c.head_dim * sizeof(float)) : 0;
+  d.ml = d.split.cluster ? 0 : round256(heads * d.split.n * sizeof(float2));
+  d.o = d.split.cluster ? 0 : round256(heads * d.split.n * c.head_dim * sizeof(float));
   d.scores = accumulate ? round256(heads * d.score_pitch * sizeof(float)) : 0;
   d.bytes = d.ml + d.o + d.scores;
   return d;
@@ -143,12 +144,10 @@ kvpop_status check_q_heads(const kvpop_paged_cache& c, int32_t n_q_heads) {
   if (n_q_heads < 1 || n_q_heads % c.n_kv_heads != 0)
     return fail(KVPOP_ERR_INVALID_ARG, "n_q_heads (%d) is not a multiple of n_kv_heads (%d)", n_q_heads, c.n_kv_heads);
   if (n_q_heads > kMaxQHeads) return fail(KVPOP_ERR_UNSUPPORTED, "at most %d query heads", kMaxQHeads);
-  // Grid sizes of the two kernels.
-  const DecodePlan d = plan_decode(c, n_q_heads, true);
-  const int64_t rows = static_cast<int64_t>(c.batch) * c.n_kv_heads;
-  if (rows * d.head_chunks >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(c.batch) * n_q_heads + rows * ((c.capacity + 511) / 512) >= (int64_t(1) << 31))
-    return fail(KVPOP_ERR_UNSUPPORTED, "too many (sequence, head, slot range) items for one launch");
+  if (n_q_heads / c.n_kv_heads > kMaxGroup)
+    return fail(KVPOP_ERR_UNSUPPORTED, "at most %d query heads per KV head", kMaxGroup);
+  if (static_cast<int64_t>(c.batch) * n_q_heads >= (int64_t(1) << 27))
+    return fail(KVPOP_ERR_UNSUPPORTED, "too many (sequence, head) items for one launch");
   return KVPOP_OK;
 }
 
@@ -278,8 +277,9 @@ kvpop_status kvpop_paged_decode_attention(const void* q, int64_t q_stride, int32
   p.n_q_heads = n_q_heads;
   p.group = n_q_heads / cache->n_kv_heads;
   p.head_chunks = d.head_chunks;
-  p.split_slots = d.split_slots;
-  p.n_split = d.n_split;
+  p.split_slots = d.split.slots;
+  p.n_split = d.split.n;
+  p.cluster = d.split.cluster;
   p.score_pitch = d.score_pitch;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const cudaError_t e = launch_paged_decode(p, cache->head_dim, cache->dtype == KVPOP_PAGED_E4M3,

@@ -24,6 +24,7 @@
 //      dim in whatever order the chunks give.
 // Chunk c of row r lies at c ^ (r & 6) ^ 4 (r & 1): both patterns touch every
 // bank once per 8 lanes.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -33,14 +34,32 @@
 
 namespace kvpop {
 
+namespace cg = cooperative_groups;
+
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
 constexpr int kPdMaxSplit = 2048;           // slots of one CTA at most
 constexpr int kPdMinPage = 8;
+constexpr int kPdMaxCluster = 16;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ void copy16(uint32_t smem, const uint8_t* p) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
+// K and V pass through the L2 once: they are the first to leave it, so that the scores written meanwhile are still
+// there for the second kernel.
+__device__ __forceinline__ uint64_t passing() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ uint64_t staying() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void store_staying(float* p, float a, float b, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(p), "f"(a), "f"(b), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t smem, const uint8_t* p, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2;" ::"r"(smem), "l"(p), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -121,7 +140,10 @@ struct Tile {
   static constexpr int kBytes = 2 * kSlots * kRow;
   static constexpr int kK = kRow / 64;                          // 16-byte chunks of a K row per lane
   static constexpr int kV = kRow >= 128 ? kRow / 128 : 1;       // 16-byte (8-byte when a row is 64) chunks of a V row
-  static constexpr int kStages = kRow == 64 ? 6 : 3;
+  // Two CTAs per SM with rings of 3 tiles where the registers allow no more, else three with 2 (4 short ones): the
+  // chain of a step is then hidden by more warps (96 x 4 e4m3 rows of 8,192 slots, no weights: 178 -> 161 us).
+  static constexpr int kStages = kRow == 64 ? 4 : kRow == 128 ? 2 : 3;
+  static constexpr int ctas(bool wide) { return wide || kRow == 256 ? 2 : 3; }
   static constexpr int kRing = kStages * kBytes;                // bytes of a warp's ring
 };
 
@@ -132,7 +154,7 @@ __device__ __forceinline__ int swizzle(int r) { return (r & 6) ^ ((r & 1) << 2);
 // lower 8 rows of the 16-row A operand are free, and the second product puts
 // the low parts of the probabilities there: both parts in one instruction.
 template <int D, bool kF8, bool kWide>
-__global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   using T = Tile<D, kF8>;
   constexpr int NT = D / 8;                 // 8-column tiles of out
   constexpr int KS = D / 16;                // k steps of q . K
@@ -146,32 +168,44 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int hc = blockIdx.x % p.head_chunks;              // chunk of 16 heads of the group
-  const int row = blockIdx.x / p.head_chunks;             // (b, h)
+  // A row's splits are a cluster, or (p.cluster == 0) CTAs of their own whose parts a second kernel joins.
+  const int item = p.cluster ? blockIdx.x / p.n_split : blockIdx.x;
+  const int split = p.cluster ? blockIdx.x % p.n_split : blockIdx.y;
+  const int hc = item % p.head_chunks;                    // chunk of 16 heads of the group
+  const int row = item / p.head_chunks;                   // (b, h)
   const int b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
-  const int split = blockIdx.y;
   const int G = min(p.group - hc * 16, 16);               // query heads of this CTA
   const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + h * p.group + hc * 16;
   const int lo = split * p.split_slots;
 
   grid_wait();
-  const int n = min(max(p.c.count[row], 0), p.c.capacity);
+  // The pages of the range's slots are on their way while the row's count is; only those in use are looked at below.
+  const int count = p.c.count[row];
+  const int e0 = lo >> p.c.page_shift;
+  const int ents = ((min(lo + p.split_slots, p.c.capacity) - 1) >> p.c.page_shift) - e0 + 1;
+  for (int i = threadIdx.x; i < ents; i += kPdThreads) pages[i] = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + e0 + i];
+  const int n = min(max(count, 0), p.c.capacity);
   const int cnt = min(n - lo, p.split_slots);             // slots of this CTA
+  // Splits with slots: those of a cluster wait for one another, the rest are gone by then (a barrier of the cluster
+  // does not wait for threads that have exited).
+  const int active = min(p.n_split, (n + p.split_slots - 1) / p.split_slots);
   if (cnt <= 0) {
     grid_launch_next();
-    for (int i = threadIdx.x; i < G; i += kPdThreads) {
-      if (p.n_split > 1) p.part_ml[(bg0 + i) * p.n_split + split] = make_float2(-INFINITY, 0.f);
-      else if (p.lse != nullptr) p.lse[bg0 + i] = -INFINITY;
-      if (p.n_split == 1 && p.scores != nullptr) p.part_ml[bg0 + i] = make_float2(-INFINITY, 0.f);
-    }
-    if (p.n_split == 1)
+    if (!p.cluster)
+      for (int i = threadIdx.x; i < G; i += kPdThreads) p.part_ml[(bg0 + i) * p.n_split + split] = make_float2(-INFINITY, 0.f);
+    if (p.cluster && split == 0) {                        // n = 0
       for (int i = threadIdx.x; i < G * D; i += kPdThreads) p.out[bg0 * D + i] = 0;
+      if (p.lse != nullptr)
+        for (int i = threadIdx.x; i < G; i += kPdThreads) p.lse[bg0 + i] = -INFINITY;
+    }
     return;
   }
-  // The pages of this CTA's slots, checked once.
-  const int e0 = lo >> p.c.page_shift;
-  const int n_ent = ((lo + cnt - 1) >> p.c.page_shift) - e0 + 1;
-  for (int i = threadIdx.x; i < n_ent; i += kPdThreads) pages[i] = page_of(p.c, b, e0 + i, p.status, DBG_PAGED_DECODE, 1);
+  // A page that the pool does not have is -1 from here on.
+  for (int i = threadIdx.x; i <= ((lo + cnt - 1) >> p.c.page_shift) - e0; i += kPdThreads)
+    if (static_cast<uint32_t>(pages[i]) >= static_cast<uint32_t>(p.c.n_pages)) {
+      pages[i] = -1;
+      debug_fail(p.status, DBG_PAGED_DECODE, 1);
+    }
 
   // q in the order of K's chunks: A operand rows g and (wide) g + 8.
   uint32_t qa[KS][kWide ? 4 : 2];
@@ -224,6 +258,7 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
   // Lane parts of the addresses: 32 lanes copy kRowsPer rows at a time, a chunk each.
   constexpr int kRowsPer = 32 / T::kChunks;
   constexpr int kSwz = T::kChunks >= 8 ? 7 : 3;           // a 64-byte row has four chunks to permute
+  const uint64_t policy = passing(), keep = staying();
   const int row_l = lane / T::kChunks, chunk_l = lane % T::kChunks;
   const uint8_t* kb = p.c.k + h * p.c.k_head + row_l * p.c.k_slot + 16 * chunk_l;
   const uint8_t* vb = p.c.v + h * p.c.v_head + row_l * p.c.v_slot + 16 * chunk_l;
@@ -254,8 +289,8 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
       for (int i = 0; i < (8 + kRowsPer - 1) / kRowsPer; ++i) {
         const int r = 8 * half + i * kRowsPer + row_l;
         const uint32_t dst = to + r * T::kRow + 16 * (chunk_l ^ (swizzle(r) & kSwz));
-        copy16(dst, kp + i * kRowsPer * p.c.k_slot);
-        copy16(dst + T::kSlots * T::kRow, vp + i * kRowsPer * p.c.v_slot);
+        copy16(dst, kp + i * kRowsPer * p.c.k_slot, policy);
+        copy16(dst + T::kSlots * T::kRow, vp + i * kRowsPer * p.c.v_slot, policy);
       }
     }
   };
@@ -318,7 +353,7 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
         float* to = p.scores + (bg0 + g + 8 * r) * p.score_pitch + lo + tile * T::kSlots + 2 * t;
 #pragma unroll
         for (int half = 0; half < T::kH; ++half)
-          *reinterpret_cast<float2*>(to + 8 * half) = make_float2(s[half][2 * r], s[half][2 * r + 1]);
+          store_staying(to + 8 * half, s[half][2 * r], s[half][2 * r + 1], keep);
       }
       y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
       y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
@@ -447,6 +482,10 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
     }
   __syncthreads();
   const float vs = kF8 && p.c.v_scale != nullptr ? p.c.v_scale[h] : 1.f;
+  // This CTA's maximum, sum and out (a row of D per head), over its warps.
+  float (*cta_o)[D] = reinterpret_cast<float (*)[D]>(rings + kPdWarps * kRows * D * sizeof(float));
+  static_assert((kPdWarps + 1) * kRows * D * 4 <= kPdWarps * T::kRing, "outputs of the warps and of the CTA");
+  __shared__ float2 cta_ml[kRows];
   for (int idx = threadIdx.x; idx < G * D; idx += kPdThreads) {
     const int i = idx / D, d = idx - i * D;
     float top = -INFINITY, sum = 0.f, acc = 0.f;
@@ -459,170 +498,285 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const __gri
       sum += sm_l[w][i] * f;
       acc += sm_o[w][i][d] * f;
     }
-    const int64_t bg = bg0 + i;
-    if (p.n_split == 1) {
-      const __nv_bfloat16 y = __float2bfloat16_rn(sum != 0.f ? acc / sum * vs : 0.f);
-      p.out[bg * D + d] = *reinterpret_cast<const uint16_t*>(&y);
-      if (d == 0) {
-        if (p.lse != nullptr) p.lse[bg] = sum != 0.f ? (top - kShift + log2f(sum)) * kLn2 : -INFINITY;
-        if (p.scores != nullptr) p.part_ml[bg] = make_float2(top - kShift, sum);
-      }
+    if (p.cluster) {
+      cta_o[i][d] = acc;
+      if (d == 0) cta_ml[i] = make_float2(top - kShift, sum);
     } else {
-      p.part_o[(bg * p.n_split + split) * D + d] = acc * vs;
-      if (d == 0) p.part_ml[bg * p.n_split + split] = make_float2(top - kShift, sum);
+      p.part_o[((bg0 + i) * p.n_split + split) * D + d] = acc * vs;
+      if (d == 0) p.part_ml[(bg0 + i) * p.n_split + split] = make_float2(top - kShift, sum);
     }
   }
+  if (!p.cluster) return;
+
+  // The cluster's active CTAs see one another's parts through distributed shared memory.
+  cg::cluster_group cluster = cg::this_cluster();
+  if (active > 1) cluster.sync();
+  else __syncthreads();
+  __shared__ float2 all_ml[kPdMaxCluster][kRows];         // then .x = the split's share of the row
+  __shared__ float lse2[kRows];                           // log2 units; +inf: nothing to add
+  for (int idx = threadIdx.x; idx < active * G; idx += kPdThreads) {
+    const int q = idx / G, i = idx - q * G;
+    all_ml[q][i] = active > 1 ? *cluster.map_shared_rank(&cta_ml[i], q) : cta_ml[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < G) {
+    const int i = threadIdx.x;
+    float top = -INFINITY, sum = 0.f;
+    for (int q = 0; q < active; ++q) top = fmaxf(top, all_ml[q][i].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    for (int q = 0; q < active; ++q) {
+      const float f = ex2(all_ml[q][i].x - base);
+      sum += all_ml[q][i].y * f;
+      all_ml[q][i].x = f;
+    }
+    const float inv = sum != 0.f ? vs / sum : 0.f;
+    for (int q = 0; q < active; ++q) all_ml[q][i].x *= inv;
+    lse2[i] = sum != 0.f ? base + log2f(sum) : INFINITY;
+    if (split == 0 && p.lse != nullptr) p.lse[bg0 + i] = sum != 0.f ? lse2[i] * kLn2 : -INFINITY;
+  }
+  __syncthreads();
+  // Each active CTA writes its share of out, two dims per thread.
+  for (int idx = split * kPdThreads + threadIdx.x; idx < G * (D / 2); idx += active * kPdThreads) {
+    const int i = idx / (D / 2), d = 2 * (idx - i * (D / 2));
+    float2 y = make_float2(0.f, 0.f);
+    const float2* from = reinterpret_cast<const float2*>(&cta_o[i][d]);
+    for (int q0 = 0; q0 < active; q0 += 8) {              // eight peers' values on their way at a time
+      float2 x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < active) x[q] = active > 1 ? *cluster.map_shared_rank(from, q0 + q) : *from;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < active) {
+          const float f = all_ml[q0 + q][i].x;
+          if (f != 0.f) y.x += x[q].x * f, y.y += x[q].y * f;
+        }
+    }
+    const __nv_bfloat162 z = __floats2bfloat162_rn(y.x, y.y);
+    *reinterpret_cast<uint32_t*>(p.out + (bg0 + i) * D + d) = *reinterpret_cast<const uint32_t*>(&z);
+  }
+  // weight[c] += sum over the group of 2^(s - lse2): this CTA's own scores, four slots (of one page) per thread.
+  if (p.scores != nullptr) {
+    for (int at = 4 * threadIdx.x; at < cnt; at += 4 * kPdThreads) {
+      const int page = pages[((lo + at) >> p.c.page_shift) - e0];
+      float add[4] = {0.f, 0.f, 0.f, 0.f};
+      const float* from = p.scores + bg0 * p.score_pitch + lo + at;
+      float* to = p.c.weight + ((static_cast<int64_t>(max(page, 0)) * p.c.n_kv_heads + h) << p.c.page_shift) + ((lo + at) & page_mask);
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (page >= 0) w = *reinterpret_cast<const float4*>(to);
+#pragma unroll
+      for (int i0 = 0; i0 < kRows; i0 += 8) {
+        float4 s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < G) s[i] = *reinterpret_cast<const float4*>(from + (i0 + i) * static_cast<int64_t>(p.score_pitch));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < G) {
+            const float z = lse2[i0 + i];
+            add[0] += ex2(s[i].x - z), add[1] += ex2(s[i].y - z), add[2] += ex2(s[i].z - z), add[3] += ex2(s[i].w - z);
+          }
+      }
+      if (page < 0) continue;
+      if (at + 3 < cnt) {
+        *reinterpret_cast<float4*>(to) = make_float4(w.x + add[0], w.y + add[1], w.z + add[2], w.w + add[3]);
+      } else {
+        const float old[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (at + e < cnt) to[e] = old[e] + add[e];
+      }
+    }
+  }
+  if (active > 1) cluster.sync();                         // the peers have read this CTA's parts
 }
 
-// Joins the splits of a row and adds the probabilities to the weights: CTAs
-// 0 .. B H_q - 1 write out and lse of one query head each, the rest take
-// kPjSlots slots of one (b, h) row.
-constexpr int kPjThreads = 128;
+// Joins the splits of a row and adds the probabilities to the weights.  CTA
+// (x, y): row x, slots y, y + gridDim.y, ... of kPjSlots each, and of the
+// group's heads those with index y modulo gridDim.y.  With lse2 of every head
+// known (a warp each), the parts and scores need one factor:
+//   out = sum over splits of part 2^(max - lse2),  weight[c] += sum over heads of 2^(score - lse2)
+// Scores were written moments ago and are mostly still in the L2; what costs
+// is the chain of loads and the few instructions per byte, so a CTA goes
+// through a whole row where there are many rows (64 x 8 rows of 4,032 slots:
+// JOIN_MEASURED).
+constexpr int kPjThreads = 256;
+constexpr int kPjWarps = kPjThreads / 32;
 constexpr int kPjSlots = 4 * kPjThreads;
-constexpr int kPjHeads = kPjThreads / 16;
+constexpr int kPjMaxGroup = 1024;
+constexpr int kPjHeads = 4;                                // heads whose scores are asked for together
 
 template <int D>
-__global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
-  constexpr int kParts = kPjThreads / (D / 4);             // splits read side by side
-  __shared__ float4 acc_s[kParts][D / 4];
-  __shared__ float red[kPjThreads / 32];
+__global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr int kWords = D / 4;                            // 16-byte words of a part's row
+  constexpr int kParts = kPjThreads / kWords;              // splits read side by side when there are many
+  __shared__ float lse2[kPjMaxGroup];                      // log2 units; +inf: nothing to add
+  __shared__ float4 acc_s[kParts][kWords];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int outs = p.n_split > 1 ? p.c.batch * p.n_q_heads : 0;
+  const int row = blockIdx.x, b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
+  const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + static_cast<int64_t>(h) * p.group;
+  const int ns = p.n_split;
   grid_wait();
   grid_launch_next();
-  const int ns = p.n_split;
-  if (static_cast<int>(blockIdx.x) < outs) {
-    const int64_t bg = blockIdx.x;
-    const float2* ml = p.part_ml + bg * ns;
-    float top = -INFINITY;
-    for (int i = tid; i < ns; i += kPjThreads) top = fmaxf(top, ml[i].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kPjThreads / 32; ++w) top = fmaxf(top, red[w]);
-    const float base = top == -INFINITY ? 0.f : top;
-    const int c = tid % (D / 4), part = tid / (D / 4);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int i = part; i < ns; i += kParts) {
-      const float2 x = ml[i];
-      if (x.x == -INFINITY && x.y == 0.f) continue;        // nothing written for an empty split
-      const float f = ex2(x.x - base);
-      const float4 y = *reinterpret_cast<const float4*>(p.part_o + (bg * ns + i) * D + 4 * c);
-      sum += x.y * f;
-      acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
-    }
-    acc_s[part][c] = acc;
-    __shared__ float sums[kParts];
-    if (c == 0) sums[part] = sum;
-    __syncthreads();
-    if (part == 0) {
-      float total = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) {
-        total += sums[i];
-        y.x += acc_s[i][c].x, y.y += acc_s[i][c].y, y.z += acc_s[i][c].z, y.w += acc_s[i][c].w;
-      }
-      const float inv = total != 0.f ? 1.f / total : 0.f;
-      const __nv_bfloat162 u = __floats2bfloat162_rn(total != 0.f ? y.x * inv : 0.f, total != 0.f ? y.y * inv : 0.f);
-      const __nv_bfloat162 w = __floats2bfloat162_rn(total != 0.f ? y.z * inv : 0.f, total != 0.f ? y.w * inv : 0.f);
-      *reinterpret_cast<uint2*>(p.out + bg * D + 4 * c) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
-      if (c == 0 && p.lse != nullptr) p.lse[bg] = total != 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
-    }
-    return;
-  }
-  // weight[c] += sum over the group of 2^(s - lse2), four slots per thread (of one page); the scores of eight heads
-  // are on their way while the warps join the splits of those heads to lse2.
-  const int chunks = (p.c.capacity + kPjSlots - 1) / kPjSlots;
-  const int id = static_cast<int>(blockIdx.x) - outs;
-  const int row = id / chunks, chunk = id - row * chunks;
-  const int b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
-  const int at = chunk * kPjSlots + 4 * tid;
-  const int page = page_of(p.c, b, at >> p.c.page_shift, nullptr, DBG_PAGED_JOIN, 1);   // reported by the attention
-  const int n = min(max(p.c.count[row], 0), p.c.capacity);
-  if (chunk * kPjSlots >= n) return;
-  const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + static_cast<int64_t>(h) * p.group;
-  __shared__ float lse2[kPjHeads];
-  float add[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int g0 = 0; g0 < p.group; g0 += kPjHeads) {
-    float4 s[kPjHeads];
+  const int count = p.c.count[row];
+  // A step's pages and scores do not depend on anything: the first step's are on their way from here on.
+  const float* scores = p.scores + bg0 * p.score_pitch;
+  const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
+  int at = blockIdx.y * kPjSlots + 4 * tid;
+  int page = -1;
+  float4 s[kPjHeads];
+  auto ask = [&](int slot, int g0) {
 #pragma unroll
     for (int i = 0; i < kPjHeads; ++i)
-      if (at < n && g0 + i < p.group)
-        s[i] = *reinterpret_cast<const float4*>(p.scores + (bg0 + g0 + i) * p.score_pitch + at);
-    __syncthreads();
-    {
-      // 16 lanes per head.
-      const int i = tid / 16, part = tid % 16;
-      float top = -INFINITY, sum = 0.f;
-      if (g0 + i < p.group)
-        for (int j = part; j < ns; j += 16) {
-          const float2 x = p.part_ml[(bg0 + g0 + i) * ns + j];
-          const float up = fmaxf(top, x.x), base = up == -INFINITY ? 0.f : up;
-          sum = sum * ex2(top - base) + x.y * ex2(x.x - base);
-          top = up;
-        }
-      float all = top;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-      all = all == -INFINITY ? 0.f : all;
-      sum *= ex2(top - all);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (part == 0) lse2[i] = sum != 0.f ? all + log2f(sum) : INFINITY;   // nothing to add
+      if (slot < p.c.capacity && g0 + i < p.group)
+        s[i] = __ldcg(reinterpret_cast<const float4*>(scores + (g0 + i) * static_cast<int64_t>(p.score_pitch) + slot));
+  };
+  if (p.scores != nullptr) {
+    if (at < p.c.capacity) page = table[at >> p.c.page_shift];
+    ask(at, 0);
+  }
+  for (int i = warp; i < p.group; i += kPjWarps) {
+    const float2* ml = p.part_ml + (bg0 + i) * ns;
+    float top = -INFINITY, sum = 0.f;
+    for (int j = lane; j < ns; j += 32) {
+      const float2 x = ml[j];
+      const float up = fmaxf(top, x.x), base = up == -INFINITY ? 0.f : up;
+      sum = sum * ex2(top - base) + x.y * ex2(x.x - base);
+      top = up;
     }
-    __syncthreads();
-    if (at < n)
+    float all = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+    all = all == -INFINITY ? 0.f : all;
+    sum *= ex2(top - all);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      lse2[i] = sum != 0.f ? all + log2f(sum) : INFINITY;
+      if (blockIdx.y == 0 && p.lse != nullptr) p.lse[bg0 + i] = sum != 0.f ? (all + log2f(sum)) * kLn2 : -INFINITY;
+    }
+  }
+  __syncthreads();
+  const int n = min(max(count, 0), p.c.capacity);
+
+  // out: splits without slots wrote no part (max -inf, sum 0).
+  auto add_split = [&](float4& acc, int64_t bg, int j, int w, float z) {
+    const float2 x = p.part_ml[bg * ns + j];
+    if (x.x == -INFINITY && x.y == 0.f) return;
+    const float f = ex2(x.x - z);
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + (bg * ns + j) * D + 4 * w));
+    acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
+  };
+  auto write_out = [&](int64_t bg, int w, const float4& y, float z) {
+    const bool some = z != INFINITY;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(some ? y.x : 0.f, some ? y.y : 0.f);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(some ? y.z : 0.f, some ? y.w : 0.f);
+    *reinterpret_cast<uint2*>(p.out + bg * D + 4 * w) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  };
+  if (ns <= kParts) {
+    // A thread per word.
+    const int heads = (p.group - static_cast<int>(blockIdx.y) + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+    for (int idx = tid; idx < heads * kWords; idx += kPjThreads) {
+      const int i = blockIdx.y + idx / kWords * gridDim.y, w = idx % kWords;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int j = 0; j < ns; ++j) add_split(acc, bg0 + i, j, w, lse2[i]);
+      write_out(bg0 + i, w, acc, lse2[i]);
+    }
+  } else {
+    // kParts threads per word, each with every kParts-th split.
+    for (int i = blockIdx.y; i < p.group; i += gridDim.y) {
+      const int w = tid % kWords, part = tid / kWords;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int j = part; j < ns; j += kParts) add_split(acc, bg0 + i, j, w, lse2[i]);
+      acc_s[part][w] = acc;
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int q = 1; q < kParts; ++q) {
+          const float4 y = acc_s[q][w];
+          acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+        }
+        write_out(bg0 + i, w, acc, lse2[i]);
+      }
+      __syncthreads();
+    }
+  }
+  if (p.scores == nullptr) return;
+
+  // weights: four slots (of one page) per thread and step.
+  const int page_mask = (1 << p.c.page_shift) - 1;
+  while (at < n) {
+    const bool good = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.c.n_pages);     // the attention reports it
+    float* to = p.c.weight + ((static_cast<int64_t>(good ? page : 0) * p.c.n_kv_heads + h) << p.c.page_shift) + (at & page_mask);
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (good) w = *reinterpret_cast<const float4*>(to);
+    const int next = at + gridDim.y * kPjSlots;
+    if (next < n) page = table[next >> p.c.page_shift];
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int g0 = 0; g0 < p.group; g0 += kPjHeads) {
+      float4 x[kPjHeads];
+#pragma unroll
+      for (int i = 0; i < kPjHeads; ++i) x[i] = s[i];
+      if (g0 + kPjHeads < p.group) ask(at, g0 + kPjHeads);
+      else ask(next, 0);
 #pragma unroll
       for (int i = 0; i < kPjHeads; ++i)
         if (g0 + i < p.group) {
-          add[0] += ex2(s[i].x - lse2[i]), add[1] += ex2(s[i].y - lse2[i]);
-          add[2] += ex2(s[i].z - lse2[i]), add[3] += ex2(s[i].w - lse2[i]);
+          const float z = lse2[g0 + i];
+          add[0] += ex2(x[i].x - z), add[1] += ex2(x[i].y - z), add[2] += ex2(x[i].z - z), add[3] += ex2(x[i].w - z);
         }
-  }
-  if (at >= n || page < 0) return;
-  float* to = p.c.weight + ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) +
-              (at & ((1 << p.c.page_shift) - 1));
-  if (at + 3 < n) {
-    float4 w = *reinterpret_cast<const float4*>(to);
-    w.x += add[0], w.y += add[1], w.z += add[2], w.w += add[3];
-    *reinterpret_cast<float4*>(to) = w;
-  } else {
+    }
+    if (good) {
+      if (at + 3 < n) {
+        *reinterpret_cast<float4*>(to) = make_float4(w.x + add[0], w.y + add[1], w.z + add[2], w.w + add[3]);
+      } else {
+        const float old[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 3; ++e)
-      if (at + e < n) to[e] += add[e];
+        for (int e = 0; e < 3; ++e)
+          if (at + e < n) to[e] = old[e] + add[e];
+      }
+    }
+    at = next;
   }
 }
 
 // Slots per CTA: enough CTAs for several rounds of two per SM, so that rows
-// of different length even out, and pieces of 128 to 2048 slots.
-int paged_split_slots(int64_t rows, int capacity) {
-  constexpr int64_t kCtas = 148 * 2 * 5;
-  int64_t slots = (rows * capacity + kCtas - 1) / kCtas;
+// of different length even out, and pieces of 128 to 2,048 slots; a second
+// kernel joins them.  Where clusters of up to 16 CTAs hold whole rows and all
+// fit at once, a row's pieces are a cluster and join in distributed shared
+// memory: one launch, and no parts in the workspace.  CLUSTER_MEASURED
+DecodeSplit paged_split(int64_t rows, int capacity, bool may_cluster) {
+  constexpr int64_t kWave = 148 * 2;
+  if (may_cluster) {
+    int n = 1;
+    while (n < kPdMaxCluster && n * 128 < capacity) n *= 2;
+    const int slots = ((capacity + n - 1) / n + 63) / 64 * 64;
+    if (rows * n <= kWave && slots <= kPdMaxSplit) return {slots, n, true};
+  }
+  int64_t slots = (rows * capacity + 5 * kWave - 1) / (5 * kWave);
   slots = std::max<int64_t>(128, std::min<int64_t>(kPdMaxSplit, (slots + 63) / 64 * 64));
-  return static_cast<int>(slots);
+  return {static_cast<int>(slots), static_cast<int>((capacity + slots - 1) / slots), false};
 }
 
 template <int D, bool kF8>
 static cudaError_t launch_decode_of(const PagedDecodeParams& p, int64_t rows, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(rows), p.n_split), block(kPdThreads);
+  const dim3 grid(static_cast<unsigned>(p.cluster ? rows * p.n_split : rows), p.cluster ? 1 : p.n_split), block(kPdThreads);
   constexpr size_t smem = kPdWarps * Tile<D, kF8>::kRing;
   static std::atomic<uint64_t> ready[2];
   auto go = [&](auto kern, int wide) {
-    const cudaError_t e = allow_smem(kern, smem, ready[wide]);
-    return e != cudaSuccess ? e : launch_paged(kern, grid, block, smem, 1, stream, p);
+    const cudaError_t e = allow_smem(kern, smem, ready[wide], true);
+    return e != cudaSuccess ? e : launch_paged(kern, grid, block, smem, p.cluster ? p.n_split : 1, stream, p);
   };
   const cudaError_t e = p.group > 8 ? go(paged_decode_kernel<D, kF8, true>, 1) : go(paged_decode_kernel<D, kF8, false>, 0);
-  if (e != cudaSuccess || (p.n_split == 1 && p.scores == nullptr)) return e;
-  int64_t join = p.n_split > 1 ? static_cast<int64_t>(p.c.batch) * p.n_q_heads : 0;
-  if (p.scores != nullptr)
-    join += static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads * ((p.c.capacity + kPjSlots - 1) / kPjSlots);
-  return launch_paged(paged_join_kernel<D>, dim3(static_cast<unsigned>(join)), dim3(kPjThreads), 0, 1, stream, p);
+  if (e != cudaSuccess || p.cluster) return e;
+  // Join: a CTA per row where that is a wave, else up to one per kPjSlots slots (or per head, without weights).
+  const int64_t kv_rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
+  const int most = p.scores != nullptr ? (p.c.capacity + kPjSlots - 1) / kPjSlots : std::min(p.group, 16);
+  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * 4 / kv_rows)));
+  return launch_paged(paged_join_kernel<D>, dim3(static_cast<unsigned>(kv_rows), parts), dim3(kPjThreads), 0, 1, stream, p);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int head_dim, bool f8, cudaStream_t stream) {

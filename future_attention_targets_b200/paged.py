@@ -16,6 +16,7 @@ lives on the device, so the loop's body can be captured in a CUDA graph and repl
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import math
@@ -42,8 +43,8 @@ class CacheStruct(ctypes.Structure):
 _P, _I32, _I64, _SIZE = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CACHE = ctypes.POINTER(CacheStruct)
 SIGS = {
-    "kvpop_paged_compact_kv": (ctypes.c_int, [_P, _P, _P, _P, _b._I32P, _I32, _CACHE, _P, _P]),
-    "kvpop_paged_append_kv": (ctypes.c_int, [_P, _P, _I64, _b._I32P, _CACHE, _I32, _I32, _P, _P, _P]),
+    "kvpop_paged_compact_kv": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _CACHE, _P, _P]),
+    "kvpop_paged_append_kv": (ctypes.c_int, [_P, _P, _I64, _P, _CACHE, _I32, _I32, _P, _P, _P]),
     "kvpop_paged_decode_workspace_bytes": (_SIZE, [_CACHE, _I32, _I32]),
     "kvpop_paged_decode_attention": (ctypes.c_int, [_P, _I64, _I32, _CACHE, ctypes.c_float, _I32, _P, _P, _P, _SIZE, _P,
                                                     _P]),
@@ -52,7 +53,7 @@ SIGS = {
 
 def paged_lib() -> ctypes.CDLL:
     """libkvpop.so with the paged cache's signatures set (they are declared beside kvpop.h's)."""
-    h = _b.lib()
+    h = _b._handle or _b.lib()
     if not getattr(h, "paged_ready", False):
         for name, (res, args) in SIGS.items():
             fn = getattr(h, name)
@@ -60,6 +61,32 @@ def paged_lib() -> ctypes.CDLL:
             fn.argtypes = args
         h.paged_ready = True
     return h
+
+
+# A call's host side is a few microseconds, so it asks torch for plain numbers instead of objects.
+
+def _raw_stream(stream, device: int) -> int:
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _b._stream_ptr(stream)
+
+
+def _host_i32(values, name: str) -> array.array:
+    """int32 offsets on the host, of a list, a numpy array or a tensor."""
+    if hasattr(values, "tolist"):
+        values = values.tolist()
+    try:
+        return array.array("i", values)
+    except OverflowError:
+        raise ValueError(f"{name}: value out of int32 range") from None
+
+
+def _check_given(t, shape, dtype, device: int, name: str):
+    import torch
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on cuda:{device}")
 
 
 def _on_stream(stream):
@@ -123,7 +150,7 @@ class PagedCache:
         if not 1 <= self.capacity <= max_pages * P:
             raise ValueError(f"capacity {self.capacity} is not within 1 .. max_pages * page_size = {max_pages * P}")
         self.batch, self.n_kv_heads, self.page_size, self.head_dim = B, H, P, d
-        self.device = dev
+        self.device, self.device_index = dev, k_pages.get_device()
         ptr = lambda t: None if t is None else t.data_ptr()
         strides = lambda t: (ctypes.c_int64 * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
         self.struct = CacheStruct(
@@ -148,46 +175,51 @@ class PagedCache:
                    k_scale=k_scale, v_scale=v_scale)
 
 
-def _rows_of(t, shape, cache, name) -> int:
+def _rows_of(t, shape, device: int, name: str) -> int:
     """The stride in elements between the first dimension's items of t (bf16, contiguous behind it), which may be
     a slice of a wider tensor such as a fused projection's output."""
     import torch
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or tuple(t.shape) != shape
-            or t.device != cache.device):
-        raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {shape} on {cache.device}")
-    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.shape != shape
+            or t.get_device() != device):
+        raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {shape} on cuda:{device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (shape[1] > 1 and s1 != shape[2]):
         raise ValueError(f"{name} must be contiguous behind its first dimension")
-    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+    return s0 if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _check_cache(cache) -> None:
+def _check_cache(cache) -> int:
+    import torch
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
-    _b._on_current_device(cache, "the cache")
+    dev = cache.device_index
+    if torch._C._cuda_getDevice() != dev:
+        _b._on_current_device(cache, "the cache")
+    return dev
 
 
 def paged_compact_kv(k, v, keep, cu_seqlens, cache: PagedCache, score=None, status=None, stream=None) -> PagedCache:
     """Fills the cache from a packed prompt: the positions with keep = 1 (keep [H_kv, T] uint8, or None for every
     position), in order, up to the capacity; weight = score [H_kv, T] (or 0).  Writes pos, weight, count and seen."""
     import torch
-    _check_cache(cache)
-    cu, cu_c = _b._cu_host(cu_seqlens)
+    dev = _check_cache(cache)
+    cu = _host_i32(cu_seqlens, "cu_seqlens")
     H, d = cache.n_kv_heads, cache.head_dim
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise TypeError("k must be a 3-D bf16 CUDA tensor [T, H_kv, d]")
     T = k.shape[0]
-    for name, t in (("k", k), ("v", v)):
-        _b._tensor(t, (T, H, d), torch.bfloat16, cache.device, name)
+    _check_given(k, (T, H, d), torch.bfloat16, dev, "k")
+    _check_given(v, (T, H, d), torch.bfloat16, dev, "v")
     if len(cu) != cache.batch + 1:
         raise ValueError(f"cu_seqlens describes {len(cu) - 1} sequences, the cache has {cache.batch}")
     if keep is not None:
-        _b._tensor(keep, (H, T), torch.uint8, cache.device, "keep")
+        _check_given(keep, (H, T), torch.uint8, dev, "keep")
     if score is not None:
-        _b._tensor(score, (H, T), torch.float32, cache.device, "score")
+        _check_given(score, (H, T), torch.float32, dev, "score")
     _b._check(paged_lib().kvpop_paged_compact_kv(
         k.data_ptr(), v.data_ptr(), None if keep is None else keep.data_ptr(),
-        None if score is None else score.data_ptr(), cu_c, T, cache.struct, _b._status_ptr(status, cache.device),
-        _b._stream_ptr(stream)))
+        None if score is None else score.data_ptr(), cu.buffer_info()[0], T, cache.struct,
+        None if status is None else _b._status_ptr(status, cache.device), _raw_stream(stream, dev)))
     return cache
 
 
@@ -197,28 +229,31 @@ def paged_append_kv(k_new, v_new, cache: PagedCache, window: int, sinks: int, cu
     sequence, over the slots of least accumulated weight where a row is full.  Returns evicted [T_new, H_kv] int32:
     the position each token displaced, -1 for a free slot, -2 if it was not stored."""
     import torch
-    _check_cache(cache)
+    dev = _check_cache(cache)
     B, H, d = cache.batch, cache.n_kv_heads, cache.head_dim
     if cu_new is None:
-        T, cu_c = B, None
+        T, cu = B, None
     else:
-        cu, cu_c = _b._cu_host(cu_new)
+        cu = _host_i32(cu_new, "cu_new")
         if len(cu) != B + 1:
             raise ValueError(f"cu_new describes {len(cu) - 1} sequences, the cache has {B}")
-        T = int(cu[-1])
-    stride = _rows_of(k_new, (T, H, d), cache, "k_new")
-    if _rows_of(v_new, (T, H, d), cache, "v_new") != stride:
+        T = cu[-1]
+    stride = _rows_of(k_new, (T, H, d), dev, "k_new")
+    if _rows_of(v_new, (T, H, d), dev, "v_new") != stride:
         raise ValueError("k_new and v_new must have the same stride between tokens")
-    if evicted is None:
+    if evicted is not None:
+        _check_given(evicted, (T, H), torch.int32, dev, "evicted")
+    elif stream is None:
+        evicted = torch.empty((T, H), dtype=torch.int32, device=cache.device)
+    else:
         with _on_stream(stream):
             evicted = torch.empty((T, H), dtype=torch.int32, device=cache.device)
-    else:
-        _b._tensor(evicted, (T, H), torch.int32, cache.device, "evicted")
     if T == 0:
         return evicted
     _b._check(paged_lib().kvpop_paged_append_kv(
-        k_new.data_ptr(), v_new.data_ptr(), stride, cu_c, cache.struct, int(window), int(sinks), evicted.data_ptr(),
-        _b._status_ptr(status, cache.device), _b._stream_ptr(stream)))
+        k_new.data_ptr(), v_new.data_ptr(), stride, None if cu is None else cu.buffer_info()[0], cache.struct, window,
+        sinks, evicted.data_ptr(), None if status is None else _b._status_ptr(status, cache.device),
+        _raw_stream(stream, dev)))
     return evicted
 
 
@@ -233,23 +268,31 @@ def paged_decode_attention(q, cache: PagedCache, scale: float | None = None, acc
     """One decode step over the cache: (out [B, H_q, d] bf16, lse [B, H_q] fp32); accumulate=True also adds each
     slot's attention weight, summed over the query heads of its KV head, to cache.weight."""
     import torch
-    _check_cache(cache)
+    dev = _check_cache(cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise TypeError("q must be a 3-D bf16 CUDA tensor [B, H_q, d]")
-    B, d, dev = cache.batch, cache.head_dim, cache.device
+    B, d = cache.batch, cache.head_dim
     Hq = q.shape[1]
-    stride = _rows_of(q, (B, Hq, d), cache, "q")
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    shape = (B, Hq, d)
+    stride = _rows_of(q, shape, dev, "q")
     h = paged_lib()
-    with contextlib.nullcontext() if stream is None else _on_stream(stream):
-        out = _b._out(out, (B, Hq, d), torch.bfloat16, dev, "out")
-        lse = _b._out(lse, (B, Hq), torch.float32, dev, "lse")
-        if workspace is None:
-            need = h.kvpop_paged_decode_workspace_bytes(cache.struct, Hq, int(accumulate))
-            workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+    with contextlib.nullcontext() if stream is None or (out is not None and lse is not None and workspace is not None) \
+            else _on_stream(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
         else:
-            workspace = _b._workspace(0, dev, workspace)
+            _check_given(out, shape, torch.bfloat16, dev, "out")
+        if lse is None:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=cache.device)
+        else:
+            _check_given(lse, (B, Hq), torch.float32, dev, "lse")
+        if workspace is None:
+            need = h.kvpop_paged_decode_workspace_bytes(cache.struct, Hq, 1 if accumulate else 0)
+            workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=cache.device)
+        elif (not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     _b._check(h.kvpop_paged_decode_attention(
-        q.data_ptr(), stride, Hq, cache.struct, scale, int(accumulate), out.data_ptr(), lse.data_ptr(),
-        workspace.data_ptr(), _b._nbytes(workspace), _b._status_ptr(status, dev), _b._stream_ptr(stream)))
+        q.data_ptr(), stride, Hq, cache.struct, 1.0 / math.sqrt(d) if scale is None else scale, 1 if accumulate else 0,
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        None if status is None else _b._status_ptr(status, cache.device), _raw_stream(stream, dev)))
     return out, lse

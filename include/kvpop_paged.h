@@ -117,7 +117,7 @@ KVPOP_API size_t kvpop_paged_decode_workspace_bytes(const kvpop_paged_cache* cac
                                                     int32_t accumulate);
 
 /* One decode step over the paged cache: for sequence b, query head g and its
- * KV head h = g / G (G = n_q_heads / n_kv_heads, any group size),
+ * KV head h = g / G (G = n_q_heads / n_kv_heads, at most 1,024),
  *   s[c]      = scale * q[b, g, :] . K[c, :],  c < n = clamp(count[b, h], 0, capacity)
  *   lse[b, g] = ln sum_c exp(s[c]),  out[b, g, :] = sum_c exp(s[c] - lse) V[c, :]
  * and, with accumulate != 0, weight[c] += sum over the group's heads of
