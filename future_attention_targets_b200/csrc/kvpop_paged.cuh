@@ -41,19 +41,21 @@ struct PagedDecodeParams {
   int64_t q_stride;       // elements between sequences
   uint16_t* out;          // bf16 [B, H_q, d]
   float* lse;             // [B, H_q] or null
-  float* part_o;          // [B * H_q, n_split, d]
-  float2* part_ml;        // [B * H_q, n_split]: running max (log2 units), sum
+  int2* item_parts;       // [items]: the first CTA that holds slots of an item, and how many do
+  float* part_o;          // [CTAs, 2, 16, d]: parts of the items that a CTA's share goes on with (0) and starts (1)
+  float2* part_ml;        // [CTAs, 2, 16]: their maxima (log2 units) and sums
+  float* row_lse2;        // [B * H_q]: lse in log2 units of items that one CTA did
   float* scores;          // [B * H_q, score_pitch], log2 units; null = weights not accumulated
   int32_t* status;
   int32_t* dbg;
-  int32_t n_q_heads, group, head_chunks, split_slots, n_split, cluster, score_pitch;   // cluster: a row's splits are one
+  int32_t n_q_heads, group, head_chunks, ctas, whole, score_pitch;   // whole: a CTA per item, and no second kernel
   float scale_log2;
 };
 
-// How a decode step's rows are cut up.
+// How a decode step's items are dealt out.
 struct DecodeSplit {
-  int slots, n;
-  bool cluster;
+  int ctas;
+  bool whole;
 };
 
 struct PagedAppendParams {
@@ -216,18 +218,16 @@ __device__ __forceinline__ void copy_rows(const PagedView& c, const uint16_t* k,
   }
 }
 
-// Raises a kernel's dynamic shared memory limit on the current device (and allows clusters of 16), once per device
-// (`done`: one bit each).
+// Raises a kernel's dynamic shared memory limit on the current device, once per device (`done`: one bit each).
 // Another thread may do it again at the same time: that changes nothing.
 template <class Kern>
-static cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<uint64_t>& done, bool wide_clusters = false) {
+static cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (dev < 64 && (done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && wide_clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }

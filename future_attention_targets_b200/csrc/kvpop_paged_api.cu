@@ -18,7 +18,7 @@ namespace kvpop {
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int head_dim, bool f8, cudaStream_t stream);
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream);
 cudaError_t launch_paged_compact(PagedCompactParams& p, int head_dim, bool f8, cudaStream_t stream);
-DecodeSplit paged_split(int64_t rows, int capacity, bool may_cluster);
+DecodeSplit paged_split(int64_t items, int capacity, int head_dim, bool f8, bool wide, bool may_be_whole);
 }  // namespace kvpop
 
 using namespace kvpop;
@@ -121,22 +121,27 @@ kvpop_status check_offsets(const int32_t* cu, int batch, const char* name) {
 struct DecodePlan {
   int head_chunks, score_pitch;
   DecodeSplit split;
-  size_t ml, o, scores, bytes;
+  size_t first, ml, o, lse2, scores, bytes;
 };
 
 DecodePlan plan_decode(const kvpop_paged_cache& c, int n_q_heads, bool accumulate) {
   DecodePlan d = {};
   const int group = n_q_heads / c.n_kv_heads;
   d.head_chunks = (group + 15) / 16;
-  const int64_t rows = static_cast<int64_t>(c.batch) * c.n_kv_heads * d.head_chunks;
+  const int64_t items = static_cast<int64_t>(c.batch) * c.n_kv_heads * d.head_chunks;
   // Heads of several chunks add to the same weights: the second kernel sums those in a fixed order.
-  d.split = paged_split(rows, c.capacity, d.head_chunks == 1 || !accumulate);
+  d.split = paged_split(items, c.capacity, c.head_dim, c.dtype == KVPOP_PAGED_E4M3, group > 8,
+                        d.head_chunks == 1 || !accumulate);
   d.score_pitch = (c.capacity + 63) / 64 * 64;
   const size_t heads = static_cast<size_t>(c.batch) * n_q_heads;
-  d.ml = d.split.cluster ? 0 : round256(heads * d.split.n * sizeof(float2));
-  d.o = d.split.cluster ? 0 : round256(heads * d.split.n * c.head_dim * sizeof(float));
+  if (!d.split.whole) {
+    d.first = round256(items * sizeof(int2));
+    d.ml = round256(static_cast<size_t>(d.split.ctas) * 2 * 16 * sizeof(float2));
+    d.o = round256(static_cast<size_t>(d.split.ctas) * 2 * 16 * c.head_dim * sizeof(float));
+    d.lse2 = accumulate ? round256(heads * sizeof(float)) : 0;
+  }
   d.scores = accumulate ? round256(heads * d.score_pitch * sizeof(float)) : 0;
-  d.bytes = d.ml + d.o + d.scores;
+  d.bytes = d.first + d.ml + d.o + d.lse2 + d.scores;
   return d;
 }
 
@@ -148,6 +153,8 @@ kvpop_status check_q_heads(const kvpop_paged_cache& c, int32_t n_q_heads) {
     return fail(KVPOP_ERR_UNSUPPORTED, "at most %d query heads per KV head", kMaxGroup);
   if (static_cast<int64_t>(c.batch) * n_q_heads >= (int64_t(1) << 27))
     return fail(KVPOP_ERR_UNSUPPORTED, "too many (sequence, head) items for one launch");
+  if (plan_decode(c, n_q_heads, true).split.ctas == 0 || plan_decode(c, n_q_heads, false).split.ctas == 0)
+    return fail(KVPOP_ERR_UNSUPPORTED, "too many slots for one launch");
   return KVPOP_OK;
 }
 
@@ -269,17 +276,18 @@ kvpop_status kvpop_paged_decode_attention(const void* q, int64_t q_stride, int32
   p.q_stride = q_stride;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  p.part_ml = reinterpret_cast<float2*>(ws);
-  p.part_o = reinterpret_cast<float*>(ws + d.ml);
-  p.scores = accumulate != 0 ? reinterpret_cast<float*>(ws + d.ml + d.o) : nullptr;
+  p.item_parts = reinterpret_cast<int2*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + d.first);
+  p.part_o = reinterpret_cast<float*>(ws + d.first + d.ml);
+  p.row_lse2 = reinterpret_cast<float*>(ws + d.first + d.ml + d.o);
+  p.scores = accumulate != 0 ? reinterpret_cast<float*>(ws + d.first + d.ml + d.o + d.lse2) : nullptr;
   p.status = dev_status;
   p.dbg = host_debug_word();
   p.n_q_heads = n_q_heads;
   p.group = n_q_heads / cache->n_kv_heads;
   p.head_chunks = d.head_chunks;
-  p.split_slots = d.split.slots;
-  p.n_split = d.split.n;
-  p.cluster = d.split.cluster;
+  p.ctas = d.split.ctas;
+  p.whole = d.split.whole;
   p.score_pitch = d.score_pitch;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const cudaError_t e = launch_paged_decode(p, cache->head_dim, cache->dtype == KVPOP_PAGED_E4M3,

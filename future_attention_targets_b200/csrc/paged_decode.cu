@@ -24,23 +24,20 @@
 //      dim in whatever order the chunks give.
 // Chunk c of row r lies at c ^ (r & 6) ^ 4 (r & 1): both patterns touch every
 // bank once per 8 lanes.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvpop_paged.cuh"
 
 namespace kvpop {
 
-namespace cg = cooperative_groups;
-
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
-constexpr int kPdMaxSplit = 2048;           // slots of one CTA at most
+constexpr int kPdChunk = 2048;              // slots whose pages are at hand
 constexpr int kPdMinPage = 8;
-constexpr int kPdMaxCluster = 16;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // K and V pass through the L2 once: they are the first to leave it, so that the scores written meanwhile are still
@@ -70,6 +67,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ uint2 lds8(uint32_t a) {
   uint2 v;
@@ -150,6 +150,24 @@ struct Tile {
 // Chunk permutation of row r within a tile.
 __device__ __forceinline__ int swizzle(int r) { return (r & 6) ^ ((r & 1) << 2); }
 
+// How the rows are dealt out.  An item is a row (b, h) and up to 16 of its
+// query heads.  It counts as its blocks of 128 slots in use, and kPdItem more
+// for what starting and ending an item costs; the items in line are cut into
+// equal shares, one per CTA, as many CTAs as the SMs hold.  So whatever the
+// rows' lengths, every CTA has the same to do and none starts for an empty row.
+// A share covers the end of one item, whole items and the start of another;
+// an item in several shares leaves parts (maximum, sum, out) for the second
+// kernel: the one that starts it in its CTA's place 1, the others in place 0.
+// Every CTA finds its share from the counts.
+constexpr int kPdBlock = 128;
+constexpr int kPdItem = 2;
+constexpr int kPdItemsHeld = 1024;          // items whose sizes a CTA keeps at hand
+
+__device__ __forceinline__ int item_slots(const PagedDecodeParams& p, int item) {
+  return min(max(p.c.count[item / p.head_chunks], 0), p.c.capacity);
+}
+__device__ __forceinline__ int size_of(int slots) { return slots > 0 ? (slots + kPdBlock - 1) / kPdBlock + kPdItem : 0; }
+
 // kWide: 9 to 16 query heads per CTA, else up to 8.  With up to 8 heads the
 // lower 8 rows of the 16-row A operand are free, and the second product puts
 // the low parts of the probabilities there: both parts in one instruction.
@@ -160,69 +178,138 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
   constexpr int KS = D / 16;                // k steps of q . K
   constexpr int kRows = kWide ? 16 : 8;     // query heads a CTA holds
   constexpr float kShift = kF8 ? 8.f : 0.f; // probabilities are held times 2^kShift: fp16's small end stays out of the way
-  __shared__ int32_t pages[kPdMaxSplit / kPdMinPage + 1];
+  __shared__ int32_t pages[2][kPdChunk / kPdMinPage + 1];   // of the chunk at work and the next
   __shared__ float sm_m[kPdWarps][kRows], sm_l[kPdWarps][kRows];
+  __shared__ int32_t share_s[2];            // first item of this CTA's share, where it begins
+  __shared__ int32_t warp_sizes[kPdWarps];
+  __shared__ int32_t slots_held[kPdItemsHeld];
+  __shared__ int32_t bad_pages;             // the segment has pages that the pool does not
+  __shared__ float2 fin[kRows];             // factor of out (1 / sum), lse2 (+inf: nothing to add)
   extern __shared__ __align__(128) uint8_t rings[];
   float (*sm_o)[kRows][D] = reinterpret_cast<float (*)[kRows][D]>(rings);   // once the rings are done with
   static_assert(kRows * D * 4 <= T::kRing, "the warps' outputs reuse their rings");
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  // A row's splits are a cluster, or (p.cluster == 0) CTAs of their own whose parts a second kernel joins.
-  const int item = p.cluster ? blockIdx.x / p.n_split : blockIdx.x;
-  const int split = p.cluster ? blockIdx.x % p.n_split : blockIdx.y;
+  const int items = p.c.batch * p.c.n_kv_heads * p.head_chunks;
+  const uint64_t policy = passing(), keep = staying();
+  if (threadIdx.x == 0) bad_pages = 0;
+  __syncthreads();
+  grid_wait();
+
+  const bool held = items <= kPdItemsHeld && !p.whole;
+  auto slots_of = [&](int i) { return held ? slots_held[i] : item_slots(p, i); };
+  int item = blockIdx.x;
+  int x = 0, x1 = 1, before = 0;            // this CTA's share of the line; where the item begins
+  if (!p.whole) {
+    // Where each thread's run of items begins, by a scan over the threads' sums.
+    const int per = (items + kPdThreads - 1) / kPdThreads;
+    const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
+    int mine = 0;
+#pragma unroll 8
+    for (int i = i0; i < i1; ++i) {
+      const int slots = item_slots(p, i);
+      mine += size_of(slots);
+      if (held) slots_held[i] = slots;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sizes[warp] = incl;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kPdWarps; ++w) {
+      if (w < warp) incl += warp_sizes[w];
+      total += warp_sizes[w];
+    }
+    const int share = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+    x = min(total, static_cast<int>(blockIdx.x) * share);   // no overflow: total + CTAs is below 2^31
+    x1 = min(total, x + share);
+    const int start = incl - mine;
+    if (start <= x && x < incl) {           // one thread's run holds the share's beginning
+      int at = start, i = i0;
+      for (int size = size_of(slots_of(i)); at + size <= x; size = size_of(slots_of(i))) at += size, ++i;
+      share_s[0] = i;
+      share_s[1] = at;
+    }
+    if (blockIdx.x == 0) {                  // for the second kernel: the CTA of each item's first slots, and how many
+      int at = start;
+      for (int i = i0; i < i1; ++i) {
+        const int size = size_of(slots_of(i));
+        const int c0 = (at + kPdItem) / share;
+        p.item_parts[i] = make_int2(c0, size > 0 ? (at + size - 1) / share - c0 + 1 : 0);
+        at += size;
+      }
+    }
+    __syncthreads();
+    if (x >= x1) return;
+    item = share_s[0];
+    before = share_s[1];
+  }
+
+  for (; x < x1; ++item) {
   const int hc = item % p.head_chunks;                    // chunk of 16 heads of the group
   const int row = item / p.head_chunks;                   // (b, h)
   const int b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
-  const int G = min(p.group - hc * 16, 16);               // query heads of this CTA
+  const int G = min(p.group - hc * 16, 16);               // query heads of this item
   const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + h * p.group + hc * 16;
-  const int lo = split * p.split_slots;
-
-  grid_wait();
-  // The pages of the range's slots are on their way while the row's count is; only those in use are looked at below.
-  const int count = p.c.count[row];
-  const int e0 = lo >> p.c.page_shift;
-  const int ents = ((min(lo + p.split_slots, p.c.capacity) - 1) >> p.c.page_shift) - e0 + 1;
-  for (int i = threadIdx.x; i < ents; i += kPdThreads) pages[i] = p.c.table[static_cast<int64_t>(b) * p.c.max_pages + e0 + i];
-  const int n = min(max(count, 0), p.c.capacity);
-  const int cnt = min(n - lo, p.split_slots);             // slots of this CTA
-  // Splits with slots: those of a cluster wait for one another, the rest are gone by then (a barrier of the cluster
-  // does not wait for threads that have exited).
-  const int active = min(p.n_split, (n + p.split_slots - 1) / p.split_slots);
-  if (cnt <= 0) {
-    grid_launch_next();
-    if (!p.cluster)
-      for (int i = threadIdx.x; i < G; i += kPdThreads) p.part_ml[(bg0 + i) * p.n_split + split] = make_float2(-INFINITY, 0.f);
-    if (p.cluster && split == 0) {                        // n = 0
+  const int n = slots_of(item);
+  int lo = 0, cnt = n;                                    // slots of this segment
+  if (!p.whole) {
+    if (n == 0) continue;
+    const int from = x - before - kPdItem, to = x1 - before - kPdItem;    // in blocks of the item
+    lo = max(0, from) * kPdBlock;
+    cnt = min(static_cast<int64_t>(n), static_cast<int64_t>(max(0, to)) * kPdBlock) - lo;
+    before += size_of(n);
+    x = before;
+    if (cnt <= 0) continue;                               // the share ends before the item's first slots
+  } else {
+    x = 1;
+    if (n == 0) {
       for (int i = threadIdx.x; i < G * D; i += kPdThreads) p.out[bg0 * D + i] = 0;
       if (p.lse != nullptr)
         for (int i = threadIdx.x; i < G; i += kPdThreads) p.lse[bg0 + i] = -INFINITY;
+      continue;
     }
-    return;
   }
-  // A page that the pool does not have is -1 from here on.
-  for (int i = threadIdx.x; i <= ((lo + cnt - 1) >> p.c.page_shift) - e0; i += kPdThreads)
-    if (static_cast<uint32_t>(pages[i]) >= static_cast<uint32_t>(p.c.n_pages)) {
-      pages[i] = -1;
-      debug_fail(p.status, DBG_PAGED_DECODE, 1);
+  // The pages of a chunk of slots; one that the pool does not have is -1 from here on.
+  const int shift = p.c.page_shift;
+  auto entry0 = [&](int chunk) { return (lo + chunk * kPdChunk) >> shift; };
+  auto stage_pages = [&](int chunk) {
+    const int e0 = entry0(chunk), e1 = (lo + min(cnt, (chunk + 1) * kPdChunk) - 1) >> shift;
+    for (int i = threadIdx.x; i <= e1 - e0; i += kPdThreads) {
+      const int page = page_of(p.c, b, e0 + i, p.status, DBG_PAGED_DECODE, 1);
+      pages[chunk & 1][i] = page;
+      if (page < 0) bad_pages = 1;
     }
+  };
+  const int chunks = (cnt + kPdChunk - 1) / kPdChunk;
 
-  // q in the order of K's chunks: A operand rows g and (wide) g + 8.
+  // q in the order of K's chunks: A operand rows g and (wide) g + 8.  Its loads and the pages' go out together.
   uint32_t qa[KS][kWide ? 4 : 2];
   float qs[kWide ? 2 : 1];                                // score per unit of product, log2 units
+  uint4 qw[kWide ? 2 : 1][D / 32];
 #pragma unroll
-  for (int r = 0; r < (kWide ? 2 : 1); ++r) {
-    const int head = g + 8 * r;
-    const uint16_t* qr = p.q + b * p.q_stride + static_cast<int64_t>(h * p.group + hc * 16 + head) * D;
-    uint32_t x[KS][2];                                    // bf16 pairs: k step s, first and second half
+  for (int r = 0; r < (kWide ? 2 : 1); ++r)
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       // bf16 cache: chunk j holds dims 32 j + 8 t + 0..7, two k steps; e4m3: dims 64 j' + 16 t + 0..15, four.
-      const int d0 = kF8 ? 64 * (j / 2) + 16 * t + 8 * (j & 1) : 32 * j + 8 * t;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (head < G) w = __ldg(reinterpret_cast<const uint4*>(qr + d0));
-      x[2 * j][0] = w.x, x[2 * j][1] = w.y, x[2 * j + 1][0] = w.z, x[2 * j + 1][1] = w.w;
+      const int d0 = kF8 ? 64 * (j / 2) + 16 * t + 8 * (j & 1) : 32 * j + 8 * t, head = g + 8 * r;
+      qw[r][j] = make_uint4(0, 0, 0, 0);
+      if (head < G)
+        qw[r][j] = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_stride + static_cast<int64_t>(h * p.group + hc * 16 + head) * D + d0));
     }
+  stage_pages(0);
+#pragma unroll
+  for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+    uint32_t x[KS][2];                                    // bf16 pairs: k step s, first and second half
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      x[2 * j][0] = qw[r][j].x, x[2 * j][1] = qw[r][j].y, x[2 * j + 1][0] = qw[r][j].z, x[2 * j + 1][1] = qw[r][j].w;
     qs[r] = p.scale_log2;
     if constexpr (kF8) {
       // fp16 q: scaled by a power of two so that its largest entry is in [1/2, 1): exact for every entry down
@@ -253,48 +340,56 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
       qa[s][(kWide ? 2 : 1) + r] = x[s][1];
     }
   }
-  __syncthreads();
-
   // Lane parts of the addresses: 32 lanes copy kRowsPer rows at a time, a chunk each.
   constexpr int kRowsPer = 32 / T::kChunks;
   constexpr int kSwz = T::kChunks >= 8 ? 7 : 3;           // a 64-byte row has four chunks to permute
-  const uint64_t policy = passing(), keep = staying();
   const int row_l = lane / T::kChunks, chunk_l = lane % T::kChunks;
-  const uint8_t* kb = p.c.k + h * p.c.k_head + row_l * p.c.k_slot + 16 * chunk_l;
-  const uint8_t* vb = p.c.v + h * p.c.v_head + row_l * p.c.v_slot + 16 * chunk_l;
-  const int page_mask = (1 << p.c.page_shift) - 1;
+  const uint32_t k_page = static_cast<uint32_t>(p.c.k_page), v_page = static_cast<uint32_t>(p.c.v_page);   // below 4 GiB
+  const uint32_t k_slot = static_cast<uint32_t>(p.c.k_slot), v_slot = static_cast<uint32_t>(p.c.v_slot);
+  const uint8_t* kb = p.c.k + h * p.c.k_head + static_cast<uint64_t>(k_slot) * row_l + 16 * chunk_l;
+  const uint8_t* vb = p.c.v + h * p.c.v_head + static_cast<uint64_t>(v_slot) * row_l + 16 * chunk_l;
+  const int page_mask = (1 << shift) - 1;
   const int tiles = (cnt + T::kSlots - 1) / T::kSlots;
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(rings)) + warp * T::kRing;
 
-  // Slots in use of each half of a tile (0 for one on a bad page).
-  auto limits = [&](int tile, int half) {
-    const int at = tile * T::kSlots + 8 * half;             // slot within this CTA's range
-    const int lim = min(max(cnt - at, 0), 8);
-    return lim > 0 && pages[((lo + at) >> p.c.page_shift) - e0] >= 0 ? lim : 0;
+  // Page of slot lo + at.
+  auto page_at = [&](int at) {
+    const int chunk = at / kPdChunk;
+    return pages[chunk & 1][((lo + at) >> shift) - entry0(chunk)];
   };
-  // Starts the copies of a tile.  A half in use is copied whole (its page holds 8 rows), one that is not stays as it
-  // is in the ring.
+  // Starts the copies of rows kFirst .. kFirst + kN - 1 of a tile, which lie on one page from slot lo + at on.  They
+  // are copied whole: a page holds them all, in use or not.
+  auto fetch_rows = [&](uint32_t to, int at, auto first, auto count) {
+    constexpr int kFirst = decltype(first)::value, kN = decltype(count)::value;
+    const int page = page_at(at);
+    if (page < 0) return;                                 // stays as it is in the ring
+    const int off = (lo + at) & page_mask;
+    const uint8_t* kp = kb + static_cast<uint64_t>(static_cast<uint32_t>(page)) * k_page + static_cast<uint64_t>(off) * k_slot;
+    const uint8_t* vp = vb + static_cast<uint64_t>(static_cast<uint32_t>(page)) * v_page + static_cast<uint64_t>(off) * v_slot;
+#pragma unroll
+    for (int i = 0; i < (kN + kRowsPer - 1) / kRowsPer; ++i) {
+      const int r = kFirst + i * kRowsPer + row_l;
+      const uint32_t dst = to + r * T::kRow + 16 * (chunk_l ^ (swizzle(r) & kSwz));
+      copy16(dst, kp + static_cast<uint64_t>(k_slot) * (i * kRowsPer), policy);
+      copy16(dst + T::kSlots * T::kRow, vp + static_cast<uint64_t>(v_slot) * (i * kRowsPer), policy);
+    }
+  };
   auto fetch = [&](int tile, int stage) {
     const uint32_t to = ring + stage * T::kBytes;
-#pragma unroll
-    for (int half = 0; half < T::kH; ++half) {
-      const int at = tile * T::kSlots + 8 * half;
-      if (at >= cnt) break;
-      const int page = pages[((lo + at) >> p.c.page_shift) - e0];
-      if (page < 0) continue;
-      const int off = (lo + at) & page_mask;
-      const uint8_t* kp = kb + page * p.c.k_page + off * p.c.k_slot;
-      const uint8_t* vp = vb + page * p.c.v_page + off * p.c.v_slot;
-#pragma unroll
-      for (int i = 0; i < (8 + kRowsPer - 1) / kRowsPer; ++i) {
-        const int r = 8 * half + i * kRowsPer + row_l;
-        const uint32_t dst = to + r * T::kRow + 16 * (chunk_l ^ (swizzle(r) & kSwz));
-        copy16(dst, kp + i * kRowsPer * p.c.k_slot, policy);
-        copy16(dst + T::kSlots * T::kRow, vp + i * kRowsPer * p.c.v_slot, policy);
+    const int at = tile * T::kSlots;
+    if ((1 << shift) >= T::kSlots) {                      // segments start at blocks, so a tile is on one page
+      fetch_rows(to, at, std::integral_constant<int, 0>(), std::integral_constant<int, T::kSlots>());
+    } else {
+      fetch_rows(to, at, std::integral_constant<int, 0>(), std::integral_constant<int, 8>());
+      if (at + 8 < cnt) fetch_rows(to, at + 8, std::integral_constant<int, 8>(), std::integral_constant<int, 8>());
+      if constexpr (T::kSlots == 32) {
+        if (at + 16 < cnt) fetch_rows(to, at + 16, std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
+        if (at + 24 < cnt) fetch_rows(to, at + 24, std::integral_constant<int, 24>(), std::integral_constant<int, 8>());
       }
     }
   };
 
+  bool has_bad = false;
   // Running state of head rows g (0) and g + 8 (1, wide): max, this lane's part of the sum, out.
   float m[kWide ? 2 : 1], l[kWide ? 2 : 1];
 #pragma unroll
@@ -307,9 +402,6 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
 
   auto compute = [&](int tile, int stage) {
     const uint32_t kt = ring + stage * T::kBytes, vt = kt + T::kSlots * T::kRow;
-    int lim[T::kH];
-#pragma unroll
-    for (int half = 0; half < T::kH; ++half) lim[half] = limits(tile, half);
     float s[T::kH][4];
 #pragma unroll
     for (int half = 0; half < T::kH; ++half) {
@@ -336,19 +428,34 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
         }
       }
     }
-    // Scale, mask, and the tile's maximum over the four lanes of a head row.
+    // Scores in log2 units.
+#pragma unroll
+    for (int half = 0; half < T::kH; ++half)
+#pragma unroll
+      for (int e = 0; e < (kWide ? 4 : 2); ++e) s[half][e] *= qs[e / 2];
+    // A tile with slots that are not in use: they score -inf, and their rows of V, which hold anything, become 0, for
+    // 0 x NaN must not reach the sums.
+    if ((tile + 1) * T::kSlots > cnt || has_bad) {
+#pragma unroll
+      for (int half = 0; half < T::kH; ++half) {
+        const int at = tile * T::kSlots + 8 * half;
+        int lim = min(max(cnt - at, 0), 8);
+        if (lim > 0 && page_at(at) < 0) lim = 0;
+#pragma unroll
+        for (int e = 0; e < (kWide ? 4 : 2); ++e)
+          if (2 * t + (e & 1) >= lim) s[half][e] = -INFINITY;
+        for (int i = lane; i < (8 - lim) * T::kChunks; i += 32)
+          sts16(vt + (8 * half + lim) * T::kRow + 16 * i, make_uint4(0, 0, 0, 0));
+      }
+      __syncwarp();
+    }
+    // The tile's maximum over the four lanes of a head row.
     float top[kWide ? 2 : 1];
 #pragma unroll
     for (int r = 0; r < (kWide ? 2 : 1); ++r) {
       float y = -INFINITY;
 #pragma unroll
-      for (int half = 0; half < T::kH; ++half)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& z = s[half][2 * r + e];
-          z = (2 * t + e < lim[half]) ? z * qs[r] : -INFINITY;
-          y = fmaxf(y, z);
-        }
+      for (int half = 0; half < T::kH; ++half) y = fmaxf(y, fmaxf(s[half][2 * r], s[half][2 * r + 1]));
       if (p.scores != nullptr && g + 8 * r < G) {
         float* to = p.scores + (bg0 + g + 8 * r) * p.score_pitch + lo + tile * T::kSlots + 2 * t;
 #pragma unroll
@@ -401,7 +508,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
     for (int kk = 0; kk < T::kH; kk += 2)
 #pragma unroll
     for (int j = 0; j < T::kV; ++j) {
-      // Rows 2t, 2t + 1, 2t + 8, 2t + 9.  Rows past the slots in use hold anything: 0 x NaN must not reach the sums.
+      // Rows 2t, 2t + 1, 2t + 8, 2t + 9.
       uint32_t w[4][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -413,7 +520,6 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
           const uint2 y = lds8(vt + rr * T::kRow + 16 * ((g >> 1) ^ (swizzle(in_half) & kSwz)) + 8 * (g & 1));
           vx.x = y.x, vx.y = y.y;
         }
-        if (in_half >= lim[kk + (r >> 1)]) vx = make_uint4(0, 0, 0, 0);
         w[r][0] = vx.x, w[r][1] = vx.y, w[r][2] = vx.z, w[r][3] = vx.w;
       }
       if constexpr (kF8) {
@@ -436,24 +542,36 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
     }
   };
 
-  // kStages - 1 tiles ahead of the one that is computed.
-#pragma unroll
-  for (int i = 0; i < T::kStages - 1; ++i) {
-    if (warp + i * kPdWarps < tiles) fetch(warp + i * kPdWarps, i);
-    copy_commit();
-  }
+  // kStages - 1 tiles ahead of the one that is computed.  The ring runs on from chunk to chunk; the barriers let the
+  // next chunk's pages in.
+  constexpr int kChunkTiles = kPdChunk / T::kSlots;
+  static_assert(kChunkTiles % kPdWarps == 0, "a chunk is the same number of steps for every warp");
   int stage = 0;
-  for (int tile = warp; tile < tiles; tile += kPdWarps) {
-    copy_wait<T::kStages - 2>();
-    __syncwarp();                                         // every lane's copies of this tile, and its reads of the last
-    const int ahead = tile + (T::kStages - 1) * kPdWarps;
-    if (ahead < tiles) fetch(ahead, stage == 0 ? T::kStages - 1 : stage - 1);
-    copy_commit();
-    compute(tile, stage);
-    stage = stage == T::kStages - 1 ? 0 : stage + 1;
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    if (chunk > 0) __syncthreads();                       // the chunk before is done with its pages
+    if (chunk + 1 < chunks) stage_pages(chunk + 1);
+    __syncthreads();
+    has_bad = bad_pages != 0;
+    if (chunk == 0) {
+#pragma unroll
+      for (int i = 0; i < T::kStages - 1; ++i) {
+        if (warp + i * kPdWarps < tiles) fetch(warp + i * kPdWarps, i);
+        copy_commit();
+      }
+    }
+    const int end = min(tiles, (chunk + 1) * kChunkTiles);
+    for (int tile = chunk * kChunkTiles + warp; tile < end; tile += kPdWarps) {
+      copy_wait<T::kStages - 2>();
+      __syncwarp();                                       // every lane's copies of this tile, and its reads of the last
+      const int ahead = tile + (T::kStages - 1) * kPdWarps;
+      if (ahead < tiles) fetch(ahead, stage == 0 ? T::kStages - 1 : stage - 1);
+      copy_commit();
+      compute(tile, stage);
+      stage = stage == T::kStages - 1 ? 0 : stage + 1;
+    }
   }
   copy_wait<0>();
-  grid_launch_next();
+  if (x >= x1) grid_launch_next();
   __syncthreads();                                        // the rings are free
 
   // Join the warps: every lane holds part of its rows' sums, all four lanes of a row the same maximum.
@@ -482,13 +600,11 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
     }
   __syncthreads();
   const float vs = kF8 && p.c.v_scale != nullptr ? p.c.v_scale[h] : 1.f;
-  // This CTA's maximum, sum and out (a row of D per head), over its warps.
-  float (*cta_o)[D] = reinterpret_cast<float (*)[D]>(rings + kPdWarps * kRows * D * sizeof(float));
-  static_assert((kPdWarps + 1) * kRows * D * 4 <= kPdWarps * T::kRing, "outputs of the warps and of the CTA");
-  __shared__ float2 cta_ml[kRows];
-  for (int idx = threadIdx.x; idx < G * D; idx += kPdThreads) {
-    const int i = idx / D, d = idx - i * D;
-    float top = -INFINITY, sum = 0.f, acc = 0.f;
+  const bool all = cnt == n;                              // the whole item: the result; else a part of it
+  const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (lo == 0 ? 1 : 0)) * 16;
+  if (threadIdx.x < G) {
+    const int i = threadIdx.x;
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kPdWarps; ++w) top = fmaxf(top, sm_m[w][i]);
     const float base = top == -INFINITY ? 0.f : top;
@@ -496,74 +612,48 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
     for (int w = 0; w < kPdWarps; ++w) {
       const float f = ex2(sm_m[w][i] - base);
       sum += sm_l[w][i] * f;
-      acc += sm_o[w][i][d] * f;
+      sm_m[w][i] = f;                                     // the warp's factor
     }
-    if (p.cluster) {
-      cta_o[i][d] = acc;
-      if (d == 0) cta_ml[i] = make_float2(top - kShift, sum);
+    const float l2 = sum != 0.f ? base - kShift + log2f(sum) : INFINITY;
+    fin[i] = make_float2(all ? (sum != 0.f ? vs / sum : 0.f) : vs, l2);
+    if (all) {
+      if (p.lse != nullptr) p.lse[bg0 + i] = sum != 0.f ? l2 * kLn2 : -INFINITY;
+      if (!p.whole && p.scores != nullptr) p.row_lse2[bg0 + i] = l2;
     } else {
-      p.part_o[((bg0 + i) * p.n_split + split) * D + d] = acc * vs;
-      if (d == 0) p.part_ml[(bg0 + i) * p.n_split + split] = make_float2(top - kShift, sum);
+      p.part_ml[part + i] = make_float2(top - kShift, sum);
     }
-  }
-  if (!p.cluster) return;
-
-  // The cluster's active CTAs see one another's parts through distributed shared memory.
-  cg::cluster_group cluster = cg::this_cluster();
-  if (active > 1) cluster.sync();
-  else __syncthreads();
-  __shared__ float2 all_ml[kPdMaxCluster][kRows];         // then .x = the split's share of the row
-  __shared__ float lse2[kRows];                           // log2 units; +inf: nothing to add
-  for (int idx = threadIdx.x; idx < active * G; idx += kPdThreads) {
-    const int q = idx / G, i = idx - q * G;
-    all_ml[q][i] = active > 1 ? *cluster.map_shared_rank(&cta_ml[i], q) : cta_ml[i];
   }
   __syncthreads();
-  if (threadIdx.x < G) {
-    const int i = threadIdx.x;
-    float top = -INFINITY, sum = 0.f;
-    for (int q = 0; q < active; ++q) top = fmaxf(top, all_ml[q][i].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    for (int q = 0; q < active; ++q) {
-      const float f = ex2(all_ml[q][i].x - base);
-      sum += all_ml[q][i].y * f;
-      all_ml[q][i].x = f;
-    }
-    const float inv = sum != 0.f ? vs / sum : 0.f;
-    for (int q = 0; q < active; ++q) all_ml[q][i].x *= inv;
-    lse2[i] = sum != 0.f ? base + log2f(sum) : INFINITY;
-    if (split == 0 && p.lse != nullptr) p.lse[bg0 + i] = sum != 0.f ? lse2[i] * kLn2 : -INFINITY;
-  }
-  __syncthreads();
-  // Each active CTA writes its share of out, two dims per thread.
-  for (int idx = split * kPdThreads + threadIdx.x; idx < G * (D / 2); idx += active * kPdThreads) {
-    const int i = idx / (D / 2), d = 2 * (idx - i * (D / 2));
-    float2 y = make_float2(0.f, 0.f);
-    const float2* from = reinterpret_cast<const float2*>(&cta_o[i][d]);
-    for (int q0 = 0; q0 < active; q0 += 8) {              // eight peers' values on their way at a time
-      float2 x[8];
+  for (int idx = threadIdx.x; idx < G * (D / 4); idx += kPdThreads) {
+    const int i = idx / (D / 4), d = 4 * (idx - i * (D / 4));
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q0 + q < active) x[q] = active > 1 ? *cluster.map_shared_rank(from, q0 + q) : *from;
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q0 + q < active) {
-          const float f = all_ml[q0 + q][i].x;
-          if (f != 0.f) y.x += x[q].x * f, y.y += x[q].y * f;
-        }
+    for (int w = 0; w < kPdWarps; ++w) {
+      const float f = sm_m[w][i];
+      const float4 z = *reinterpret_cast<const float4*>(&sm_o[w][i][d]);
+      y.x += z.x * f, y.y += z.y * f, y.z += z.z * f, y.w += z.w * f;
     }
-    const __nv_bfloat162 z = __floats2bfloat162_rn(y.x, y.y);
-    *reinterpret_cast<uint32_t*>(p.out + (bg0 + i) * D + d) = *reinterpret_cast<const uint32_t*>(&z);
+    const float f = fin[i].x;
+    if (all) {
+      const bool some = fin[i].y != INFINITY;
+      const __nv_bfloat162 u = __floats2bfloat162_rn(some ? y.x * f : 0.f, some ? y.y * f : 0.f);
+      const __nv_bfloat162 w = __floats2bfloat162_rn(some ? y.z * f : 0.f, some ? y.w * f : 0.f);
+      *reinterpret_cast<uint2*>(p.out + (bg0 + i) * D + d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (part + i) * D + d) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+    }
   }
-  // weight[c] += sum over the group of 2^(s - lse2): this CTA's own scores, four slots (of one page) per thread.
-  if (p.scores != nullptr) {
-    for (int at = 4 * threadIdx.x; at < cnt; at += 4 * kPdThreads) {
-      const int page = pages[((lo + at) >> p.c.page_shift) - e0];
+  // A whole item of a call without the second kernel: weight[c] += sum over its heads of 2^(s - lse2), four slots (of
+  // one page) per thread, from the scores that this CTA wrote.
+  if (p.whole && p.scores != nullptr) {
+    for (int at = 4 * threadIdx.x; at < n; at += 4 * kPdThreads) {
+      const int page = page_at(at);
+      if (page < 0) continue;
+      float* to = p.c.weight + ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << shift) + (at & page_mask);
+      const float* from = p.scores + bg0 * p.score_pitch + at;
+      const float4 w = *reinterpret_cast<const float4*>(to);
       float add[4] = {0.f, 0.f, 0.f, 0.f};
-      const float* from = p.scores + bg0 * p.score_pitch + lo + at;
-      float* to = p.c.weight + ((static_cast<int64_t>(max(page, 0)) * p.c.n_kv_heads + h) << p.c.page_shift) + ((lo + at) & page_mask);
-      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (page >= 0) w = *reinterpret_cast<const float4*>(to);
 #pragma unroll
       for (int i0 = 0; i0 < kRows; i0 += 8) {
         float4 s[8];
@@ -573,22 +663,23 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i0 + i < G) {
-            const float z = lse2[i0 + i];
+            const float z = fin[i0 + i].y;
             add[0] += ex2(s[i].x - z), add[1] += ex2(s[i].y - z), add[2] += ex2(s[i].z - z), add[3] += ex2(s[i].w - z);
           }
       }
-      if (page < 0) continue;
-      if (at + 3 < cnt) {
+      if (at + 3 < n) {
         *reinterpret_cast<float4*>(to) = make_float4(w.x + add[0], w.y + add[1], w.z + add[2], w.w + add[3]);
       } else {
         const float old[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 3; ++e)
-          if (at + e < cnt) to[e] = old[e] + add[e];
+          if (at + e < n) to[e] = old[e] + add[e];
       }
     }
   }
-  if (active > 1) cluster.sync();                         // the peers have read this CTA's parts
+  if (threadIdx.x == 0) bad_pages = 0;                    // read by all before the last barrier
+  __syncthreads();                                        // before the next item's pages, rings and factors
+  }
 }
 
 // Joins the splits of a row and adds the probabilities to the weights.  CTA
@@ -615,7 +706,6 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x, b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
   const int64_t bg0 = static_cast<int64_t>(b) * p.n_q_heads + static_cast<int64_t>(h) * p.group;
-  const int ns = p.n_split;
   grid_wait();
   grid_launch_next();
   const int count = p.c.count[row];
@@ -635,74 +725,65 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
     if (at < p.c.capacity) page = table[at >> p.c.page_shift];
     ask(at, 0);
   }
+  // Parts of head i's item: of CTAs x .. x + y - 1, the first in place 1.
+  auto parts_of = [&](int i) { return p.item_parts[row * p.head_chunks + i / 16]; };
+  auto part_at = [&](const int2& q, int i, int j) { return (static_cast<int64_t>(q.x + j) * 2 + (j == 0 ? 1 : 0)) * 16 + i % 16; };
   for (int i = warp; i < p.group; i += kPjWarps) {
-    const float2* ml = p.part_ml + (bg0 + i) * ns;
-    float top = -INFINITY, sum = 0.f;
-    for (int j = lane; j < ns; j += 32) {
-      const float2 x = ml[j];
-      const float up = fmaxf(top, x.x), base = up == -INFINITY ? 0.f : up;
-      sum = sum * ex2(top - base) + x.y * ex2(x.x - base);
-      top = up;
-    }
-    float all = top;
+    const int2 q = parts_of(i);
+    float l2 = INFINITY;
+    if (q.y == 1) {
+      if (p.scores != nullptr) l2 = p.row_lse2[bg0 + i];
+    } else {
+      float top = -INFINITY, sum = 0.f;
+      for (int j = lane; j < q.y; j += 32) {
+        const float2 x = p.part_ml[part_at(q, i, j)];
+        const float up = fmaxf(top, x.x), base = up == -INFINITY ? 0.f : up;
+        sum = sum * ex2(top - base) + x.y * ex2(x.x - base);
+        top = up;
+      }
+      float all = top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-    all = all == -INFINITY ? 0.f : all;
-    sum *= ex2(top - all);
+      for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+      all = all == -INFINITY ? 0.f : all;
+      sum *= ex2(top - all);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      lse2[i] = sum != 0.f ? all + log2f(sum) : INFINITY;
-      if (blockIdx.y == 0 && p.lse != nullptr) p.lse[bg0 + i] = sum != 0.f ? (all + log2f(sum)) * kLn2 : -INFINITY;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (sum != 0.f) l2 = all + log2f(sum);
+      if (lane == 0 && blockIdx.y == 0 && p.lse != nullptr) p.lse[bg0 + i] = sum != 0.f ? l2 * kLn2 : -INFINITY;
     }
+    if (lane == 0) lse2[i] = l2;
   }
   __syncthreads();
   const int n = min(max(count, 0), p.c.capacity);
 
-  // out: splits without slots wrote no part (max -inf, sum 0).
-  auto add_split = [&](float4& acc, int64_t bg, int j, int w, float z) {
-    const float2 x = p.part_ml[bg * ns + j];
-    if (x.x == -INFINITY && x.y == 0.f) return;
-    const float f = ex2(x.x - z);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + (bg * ns + j) * D + 4 * w));
-    acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
-  };
-  auto write_out = [&](int64_t bg, int w, const float4& y, float z) {
-    const bool some = z != INFINITY;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(some ? y.x : 0.f, some ? y.y : 0.f);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(some ? y.z : 0.f, some ? y.w : 0.f);
-    *reinterpret_cast<uint2*>(p.out + bg * D + 4 * w) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  };
-  if (ns <= kParts) {
-    // A thread per word.
-    const int heads = (p.group - static_cast<int>(blockIdx.y) + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
-    for (int idx = tid; idx < heads * kWords; idx += kPjThreads) {
-      const int i = blockIdx.y + idx / kWords * gridDim.y, w = idx % kWords;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // out of this CTA's heads, kParts threads per word, each with every kParts-th part.
+  for (int i = blockIdx.y; i < p.group; i += gridDim.y) {
+    const int2 q = parts_of(i);
+    if (q.y == 1) continue;                            // the attention wrote it
+    const int w = tid % kWords, part = tid / kWords;
+    const float z = lse2[i];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (z != INFINITY) {
 #pragma unroll 4
-      for (int j = 0; j < ns; ++j) add_split(acc, bg0 + i, j, w, lse2[i]);
-      write_out(bg0 + i, w, acc, lse2[i]);
-    }
-  } else {
-    // kParts threads per word, each with every kParts-th split.
-    for (int i = blockIdx.y; i < p.group; i += gridDim.y) {
-      const int w = tid % kWords, part = tid / kWords;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int j = part; j < ns; j += kParts) add_split(acc, bg0 + i, j, w, lse2[i]);
-      acc_s[part][w] = acc;
-      __syncthreads();
-      if (part == 0) {
-#pragma unroll
-        for (int q = 1; q < kParts; ++q) {
-          const float4 y = acc_s[q][w];
-          acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
-        }
-        write_out(bg0 + i, w, acc, lse2[i]);
+      for (int j = part; j < q.y; j += kParts) {
+        const int64_t from = part_at(q, i, j);
+        const float f = ex2(p.part_ml[from].x - z);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + 4 * w));
+        acc.x += y.x * f, acc.y += y.y * f, acc.z += y.z * f, acc.w += y.w * f;
       }
-      __syncthreads();
     }
+    acc_s[part][w] = acc;
+    __syncthreads();
+    if (part == 0) {
+      for (int o = 1; o < min(kParts, q.y); ++o) {
+        const float4 y = acc_s[o][w];
+        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+      }
+      const __nv_bfloat162 u = __floats2bfloat162_rn(acc.x, acc.y), v = __floats2bfloat162_rn(acc.z, acc.w);
+      *reinterpret_cast<uint2*>(p.out + (bg0 + i) * D + 4 * w) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+    }
+    __syncthreads();
   }
   if (p.scores == nullptr) return;
 
@@ -743,46 +824,39 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
   }
 }
 
-// Slots per CTA: enough CTAs for several rounds of two per SM, so that rows
-// of different length even out, and pieces of 128 to 2,048 slots; a second
-// kernel joins them.  Where clusters of up to 16 CTAs hold whole rows and all
-// fit at once, a row's pieces are a cluster and join in distributed shared
-// memory: one launch, and no parts in the workspace.  CLUSTER_MEASURED
-DecodeSplit paged_split(int64_t rows, int capacity, bool may_cluster) {
-  constexpr int64_t kWave = 148 * 2;
-  if (may_cluster) {
-    int n = 1;
-    while (n < kPdMaxCluster && n * 128 < capacity) n *= 2;
-    const int slots = ((capacity + n - 1) / n + 63) / 64 * 64;
-    if (rows * n <= kWave && slots <= kPdMaxSplit) return {slots, n, true};
-  }
-  int64_t slots = (rows * capacity + 5 * kWave - 1) / (5 * kWave);
-  slots = std::max<int64_t>(128, std::min<int64_t>(kPdMaxSplit, (slots + 63) / 64 * 64));
-  return {static_cast<int>(slots), static_cast<int>((capacity + slots - 1) / slots), false};
+// Whole items, one CTA each and no second kernel, where rows are short
+// (WHOLE_MEASURED); else as many shares as CTAs fit on 148 SMs; 0 CTAs: too
+// many.
+DecodeSplit paged_split(int64_t items, int capacity, int head_dim, bool f8, bool wide, bool may_be_whole) {
+  if (may_be_whole && capacity <= 512) return {static_cast<int>(items), true};
+  const int per_sm = head_dim == 128 ? (f8 ? Tile<128, true>::ctas(wide) : Tile<128, false>::ctas(wide))
+                                     : (f8 ? Tile<64, true>::ctas(wide) : Tile<64, false>::ctas(wide));
+  const int64_t sizes = items * ((capacity + kPdBlock - 1) / kPdBlock + kPdItem);
+  if (sizes + 148 * per_sm >= (int64_t(1) << 31)) return {0, false};    // the line's places are 32-bit
+  return {static_cast<int>(std::min<int64_t>(sizes, 148 * per_sm)), false};
 }
 
 template <int D, bool kF8>
-static cudaError_t launch_decode_of(const PagedDecodeParams& p, int64_t rows, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.cluster ? rows * p.n_split : rows), p.cluster ? 1 : p.n_split), block(kPdThreads);
+static cudaError_t launch_decode_of(const PagedDecodeParams& p, cudaStream_t stream) {
+  const dim3 grid(p.ctas), block(kPdThreads);
   constexpr size_t smem = kPdWarps * Tile<D, kF8>::kRing;
   static std::atomic<uint64_t> ready[2];
   auto go = [&](auto kern, int wide) {
-    const cudaError_t e = allow_smem(kern, smem, ready[wide], true);
-    return e != cudaSuccess ? e : launch_paged(kern, grid, block, smem, p.cluster ? p.n_split : 1, stream, p);
+    const cudaError_t e = allow_smem(kern, smem, ready[wide]);
+    return e != cudaSuccess ? e : launch_paged(kern, grid, block, smem, 1, stream, p);
   };
   const cudaError_t e = p.group > 8 ? go(paged_decode_kernel<D, kF8, true>, 1) : go(paged_decode_kernel<D, kF8, false>, 0);
-  if (e != cudaSuccess || p.cluster) return e;
+  if (e != cudaSuccess || p.whole) return e;
   // Join: a CTA per row where that is a wave, else up to one per kPjSlots slots (or per head, without weights).
-  const int64_t kv_rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
+  const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const int most = p.scores != nullptr ? (p.c.capacity + kPjSlots - 1) / kPjSlots : std::min(p.group, 16);
-  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * 4 / kv_rows)));
-  return launch_paged(paged_join_kernel<D>, dim3(static_cast<unsigned>(kv_rows), parts), dim3(kPjThreads), 0, 1, stream, p);
+  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * 4 / rows)));
+  return launch_paged(paged_join_kernel<D>, dim3(static_cast<unsigned>(rows), parts), dim3(kPjThreads), 0, 1, stream, p);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int head_dim, bool f8, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads * p.head_chunks;
-  if (head_dim == 128) return f8 ? launch_decode_of<128, true>(p, rows, stream) : launch_decode_of<128, false>(p, rows, stream);
-  return f8 ? launch_decode_of<64, true>(p, rows, stream) : launch_decode_of<64, false>(p, rows, stream);
+  if (head_dim == 128) return f8 ? launch_decode_of<128, true>(p, stream) : launch_decode_of<128, false>(p, stream);
+  return f8 ? launch_decode_of<64, true>(p, stream) : launch_decode_of<64, false>(p, stream);
 }
 
 }  // namespace kvpop
