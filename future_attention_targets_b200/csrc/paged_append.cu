@@ -51,6 +51,37 @@ __device__ __forceinline__ Candidate first_to_go(const Candidate& c) {
   return r;
 }
 
+// A warp writes token `tok` of the call, position `seen` of sequence b, into `slot` of row (b, h) (< 0: there is none
+// for it), where position `old` goes (-1: nothing does); `fresh` is the lane's 16-byte word of its K row, then V's.
+template <int D, bool kF8>
+__device__ __forceinline__ void write_one(const PagedAppendParams& p, int b, int h, int tok, int slot, int old, int seen,
+                                          const uint4& fresh) {
+  const int lane = threadIdx.x & 31;
+  const int off = slot & ((1 << p.c.page_shift) - 1);
+  int page = -1;
+  if (slot < 0) debug_fail(p.status, DBG_PAGED_APPEND, 3);
+  else page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 2);
+  if (lane == 0 && p.evicted != nullptr) p.evicted[static_cast<int64_t>(tok) * p.c.n_kv_heads + h] = page >= 0 ? old : -2;
+  if (page < 0) return;
+  if (lane == 0) {
+    const int64_t at = ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) + off;
+    p.c.pos[at] = seen;
+    p.c.weight[at] = 0.f;
+  }
+  if (lane < D / 4) {
+    const bool is_v = lane >= D / 8;
+    const int word = lane % (D / 8);
+    uint8_t* to = is_v ? p.c.v + page * p.c.v_page + h * p.c.v_head + off * p.c.v_slot
+                       : p.c.k + page * p.c.k_page + h * p.c.k_head + off * p.c.k_slot;
+    if constexpr (kF8) {
+      const float* scale = is_v ? p.c.v_scale : p.c.k_scale;
+      *reinterpret_cast<uint2*>(to + 8 * word) = to_e4m3x8(fresh, divisor_of(scale != nullptr ? scale[h] : 1.f));
+    } else {
+      *reinterpret_cast<uint4*>(to + 16 * word) = fresh;
+    }
+  }
+}
+
 template <int D, bool kF8, bool kChunk>
 __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
     paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
@@ -234,30 +265,10 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
     else __syncthreads();
     if (cta != 0) return;
     if (warp > 0) return;
-    int page = -1;
-    const int off = slot & page_mask;
-    if (slot >= 0) page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 2);
-    else debug_fail(p.status, DBG_PAGED_APPEND, 3);
+    write_one<D, kF8>(p, b, h, tok0, slot, old, seen, fresh);
     if (lane == 0) {
       p.c.count[row] = min(n + 1, cap);
       p.c.seen[row] = seen + 1;
-      if (p.evicted != nullptr) p.evicted[static_cast<int64_t>(tok0) * p.c.n_kv_heads + h] = page >= 0 ? old : -2;
-      if (page >= 0) {
-        p.c.pos[meta_at(page, off)] = seen;
-        p.c.weight[meta_at(page, off)] = 0.f;
-      }
-    }
-    if (page >= 0 && lane < D / 4) {
-      const bool is_v = lane >= D / 8;
-      const int word = lane % (D / 8);
-      uint8_t* to = is_v ? p.c.v + page * p.c.v_page + h * p.c.v_head + off * p.c.v_slot
-                         : p.c.k + page * p.c.k_page + h * p.c.k_head + off * p.c.k_slot;
-      if constexpr (kF8) {
-        const float* scale = is_v ? p.c.v_scale : p.c.k_scale;
-        *reinterpret_cast<uint2*>(to + 8 * word) = to_e4m3x8(fresh, divisor_of(scale != nullptr ? scale[h] : 1.f));
-      } else {
-        *reinterpret_cast<uint4*>(to + 16 * word) = fresh;
-      }
     }
   } else {
     // Rows to write, up to kPaList at a time, where the histograms are at other times.
@@ -485,6 +496,180 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   }
 }
 
+// One token into each of many rows: the argmin of paged_append_kernel as a
+// stream.  A CTA takes every gridDim.x-th row in steps of kPsSlots slots; while
+// it looks at one step's weights and positions, the next one's, and the page
+// numbers, counts and new rows of the one after that, are on their way into
+// shared memory, so the SM always has bytes in flight and no load is waited for
+// (256 x 8 rows of 4,032 slots: 23.9 us with a CTA per row, STREAM_MEASURED).
+// A thread reads what it copied itself; the barrier of a row's end shows warp 0
+// the rest.
+constexpr int kPsThreads = 256;
+constexpr int kPsWarps = kPsThreads / 32;
+constexpr int kPsU = 4;                                   // 16-byte words of weights (and positions) of a thread
+constexpr int kPsSlots = 4 * kPsThreads * kPsU;
+
+struct StreamSmem {
+  uint4 words[2][2][kPsU][kPsThreads];                    // [step parity][weights, positions]
+  int32_t pages[2][kPsU][kPsThreads];
+  int32_t row[3][kPsWarps][2];                            // count and seen, a copy per warp
+  uint4 fresh[3][32];                                     // the new K and V row, for warp 0
+  Candidate best[2][kPsWarps];
+};
+
+__device__ __forceinline__ void copy16_to(void* smem, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void copy4_to(void* smem, const void* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(p)
+               : "memory");
+}
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kPsThreads, 3) paged_append_stream_kernel(const __grid_constant__ PagedAppendParams p) {
+  extern __shared__ __align__(16) uint8_t stream_smem[];
+  StreamSmem& sm = *reinterpret_cast<StreamSmem*>(stream_smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = p.c.n_kv_heads, rows = p.c.batch * heads, cap = p.c.capacity;
+  const int steps = (cap + kPsSlots - 1) / kPsSlots;      // of a row
+  const int page_mask = (1 << p.c.page_shift) - 1;
+  grid_wait();
+  grid_launch_next();
+
+  // A step of a row, and the ones after it.
+  struct Step {
+    int row, b, h, part;
+  };
+  auto advance = [&](Step& u) {
+    if (++u.part < steps) return;
+    u.part = 0;
+    u.row += gridDim.x;
+    u.b = u.row / heads;
+    u.h = u.row - u.b * heads;
+  };
+  // Pages and counts, and with a row's last step its new rows.
+  auto ask_meta = [&](const Step& u, int at, int parity) {
+    if (u.row >= rows) return;
+    const int32_t* table = p.c.table + static_cast<int64_t>(u.b) * p.c.max_pages;
+#pragma unroll
+    for (int i = 0; i < kPsU; ++i) {
+      const int s = u.part * kPsSlots + 4 * (tid + i * kPsThreads);
+      if (s < cap) copy4_to(&sm.pages[parity][i][tid], table + (s >> p.c.page_shift));
+    }
+    if (lane < 2) copy4_to(&sm.row[at][warp][lane], (lane == 0 ? p.c.count : p.c.seen) + u.row);
+    if (warp == 0 && lane < D / 4 && u.part == steps - 1) {
+      const uint16_t* from = (lane < D / 8 ? p.k_new : p.v_new) + u.b * p.token_stride + static_cast<int64_t>(u.h) * D + 8 * (lane % (D / 8));
+      copy16_to(&sm.fresh[at][lane], from);
+    }
+  };
+  auto meta_at = [&](int page, int h, int off) {
+    return ((static_cast<int64_t>(page) * heads + h) << p.c.page_shift) + off;
+  };
+  // Words that a step has to look at, a bit each: none while the row has a free slot, or takes no part.
+  auto ask_words = [&](const Step& u, int at, int parity) {
+    int here = 0;
+    if (u.row >= rows || sm.row[at][warp][0] < cap) return here;
+#pragma unroll
+    for (int i = 0; i < kPsU; ++i) {
+      const int s = u.part * kPsSlots + 4 * (tid + i * kPsThreads);
+      if (s >= cap) continue;
+      const int page = sm.pages[parity][i][tid];
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.n_pages)) {
+        debug_fail(p.status, DBG_PAGED_APPEND, 1);
+        continue;
+      }
+      const int64_t from = meta_at(page, u.h, s & page_mask);
+      copy16_to(&sm.words[parity][0][i][tid], p.c.weight + from);
+      copy16_to(&sm.words[parity][1][i][tid], p.c.pos + from);
+      here |= 1 << i;
+    }
+    return here;
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  auto landed = [] {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();                                         // count and seen are two lanes' copies
+  };
+
+  Step now = {static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.x) / heads, static_cast<int>(blockIdx.x) % heads, 0};
+  Step next = now;
+  advance(next);
+  ask_meta(now, 0, 0);
+  commit();
+  landed();
+  int here = ask_words(now, 0, 0);
+  ask_meta(next, 1, 1);
+  commit();
+  Candidate c = {~0u, -1, -1};
+  int at = 0, parity = 0, best_at = 0;                    // of the step at hand
+  while (now.row < rows) {
+    landed();                                             // this step's words, the next one's pages and counts
+    Step after = next;
+    if (next.row < rows) advance(after);
+    const int at1 = at == 2 ? 0 : at + 1, at2 = at1 == 2 ? 0 : at1 + 1;
+    const int here_next = ask_words(next, at1, parity ^ 1);
+    ask_meta(after, at2, parity);                         // this step's pages are done with
+    commit();
+    const int count = sm.row[at][warp][0], seen = sm.row[at][warp][1];
+    if (count >= cap) {
+      const int64_t recent = static_cast<int64_t>(seen) + 1 - p.window;
+      const uint32_t span = static_cast<uint32_t>(max(int64_t(0), min(recent, int64_t(1) << 31) - p.sinks));
+#pragma unroll
+      for (int i = 0; i < kPsU; ++i) {
+        if (((here >> i) & 1) == 0) continue;
+        const int s = now.part * kPsSlots + 4 * (tid + i * kPsThreads);
+        const uint4 w = sm.words[parity][0][i][tid], x = sm.words[parity][1][i][tid];
+        const uint32_t wu[4] = {w.x, w.y, w.z, w.w};
+        int xi[4] = {static_cast<int>(x.x), static_cast<int>(x.y), static_cast<int>(x.z), static_cast<int>(x.w)};
+        if (s + 3 >= cap) {
+          xi[3] = -1;
+          if (s + 2 >= cap) xi[2] = -1;
+          if (s + 1 >= cap) xi[1] = -1;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool goes = static_cast<uint32_t>(xi[e]) - static_cast<uint32_t>(p.sinks) < span;
+          const uint32_t k = goes ? weight_key(__uint_as_float(wu[e])) : ~0u;
+          const bool better = (k < c.key) | ((k == c.key) & (xi[e] > c.pos) & goes);
+          c.key = better ? k : c.key;
+          c.pos = better ? xi[e] : c.pos;
+          c.at = better ? s + e : c.at;
+        }
+      }
+    }
+    if (now.part == steps - 1) {                          // the row's last step
+      c = first_to_go(c);
+      if (lane == 0) sm.best[best_at][warp] = c;
+      __syncthreads();
+      if (warp == 0) {
+        c = lane < kPsWarps ? sm.best[best_at][lane] : Candidate{~0u, -1, -1};
+        c = first_to_go(c);
+        if (count < 0) {
+          if (lane == 0 && p.evicted != nullptr) p.evicted[static_cast<int64_t>(now.b) * heads + now.h] = -2;
+        } else {
+          const int slot = count < cap ? count : c.key == ~0u ? -1 : c.at;
+          write_one<D, kF8>(p, now.b, now.h, now.b, slot, count < cap ? -1 : c.pos, seen, sm.fresh[at][lane]);
+          if (lane == 0) {
+            p.c.count[now.row] = min(count + 1, cap);
+            p.c.seen[now.row] = seen + 1;
+          }
+        }
+      }
+      c = {~0u, -1, -1};
+      best_at ^= 1;                                       // its other buffer was read before the last barrier
+    }
+    now = next;
+    next = after;
+    here = here_next;
+    at = at1;
+    parity ^= 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+constexpr int kPsRows = 3 * 148;     // more rows than this are streamed
+
 // CTAs per row.  One out: the largest of 8, 4, 2, 1 whose clusters leave two
 // CTAs per SM at most and 1,024 slots per CTA at least.  Several out: the
 // fewest that leave slices of 8,192 slots at most, and more while the CTAs do
@@ -494,6 +679,18 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const bool chunk = !p.one_each;
+  if (!chunk && rows > kPsRows) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows, 3 * 148))), block(kPsThreads);
+    constexpr size_t kPsSmem = sizeof(StreamSmem);
+    static std::atomic<uint64_t> ready[4];
+    auto go = [&](auto kern, int which) {
+      const cudaError_t e = allow_smem(kern, kPsSmem, ready[which]);
+      return e != cudaSuccess ? e : launch_paged(kern, grid, block, kPsSmem, 1, stream, p);
+    };
+    if (head_dim == 128)
+      return f8 ? go(paged_append_stream_kernel<128, true>, 0) : go(paged_append_stream_kernel<128, false>, 1);
+    return f8 ? go(paged_append_stream_kernel<64, true>, 2) : go(paged_append_stream_kernel<64, false>, 3);
+  }
   int ctas = 1;
   if (chunk) {
     while (ctas < 8 && (p.c.capacity > 8192 * ctas || (rows * ctas < 148 && p.c.capacity > 2048 * ctas))) ctas <<= 1;

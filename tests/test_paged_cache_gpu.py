@@ -287,6 +287,39 @@ def test_append_one(B, H, d, page, cap, counts, window, sinks, dtype, layout):
         check_append(a, None, window, sinks, seed=step, fused=step % 2 == 1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_append_one_to_many_rows(dtype):
+    """More rows than CTAs, each in several steps, full ones beside ones with room and ones that take no part."""
+    B, H, cap = 150, 3, 4500
+    counts = [[(cap, cap, cap - 1, 17, -1, 0, cap)[(b * H + h) % 7] for h in range(H)] for b in range(B)]
+    a = ref.make_cache(B, H, 64, 64, cap, dtype, "phd", seed=cap)
+    g = gen(3)
+    page_count = a["pos"].shape[0]
+    a["weight"].copy_(torch.randint(0, 500, (page_count, H, 64), generator=g).float())     # many equal weights
+    a["pos"].copy_(torch.randint(0, 9000, (page_count, H, 64), generator=g).to(torch.int32))
+    a["count"].copy_(torch.tensor(counts))
+    a["seen"].fill_(9000)
+    for name in ("k_pages", "v_pages"):
+        a[name].view(torch.uint8).zero_()
+    a["page_table"][5, 30] = -1                               # a hole in one full sequence
+    before = a["page_table"].clone()
+    a["page_table"][5, 30] = before[6, 0]                     # the reference: the hole's slots may not go
+    hole = dict(a, page_table=a["page_table"].clone(), pos=a["pos"].clone())
+    a["page_table"].copy_(before)
+    x = torch.randn(B, 2 * H, 64, generator=g).to(torch.bfloat16)
+    rows = [b for b in range(B) if b != 5]
+    want, evicted = ref.append(hole, x[:, :H], x[:, H:], list(range(B + 1)), 256, 4)
+    got = kv.paged_append_kv(x[:, :H].cuda().contiguous(), x[:, H:].cuda().contiguous(), kv.PagedCache(**a), 256, 4)
+    torch.cuda.synchronize()
+    assert np.array_equal(got.cpu().numpy()[rows], evicted[rows])
+    for b in rows:
+        t = before[b].long().cpu()
+        for name in ("k_pages", "v_pages", "pos", "weight"):
+            assert np.array_equal(ref.as_bytes(a[name].view(torch.uint8)[t] if a[name].dtype == ref.E4M3 else a[name][t]),
+                                  ref.as_bytes(want[name].view(torch.uint8)[t] if a[name].dtype == ref.E4M3 else want[name][t])), (b, name)
+    assert np.array_equal(a["count"].cpu().numpy(), want["count"].numpy())
+
+
 @pytest.mark.parametrize("B,H,d,page,cap,counts,m,window,sinks,dtype", [
     (2, 2, 64, 16, 100, [[100, 90], [0, 97]], [8, 5], 8, 4, "bf16"),
     (3, 1, 128, 8, 64, [[64], [64], [10]], [32, 0, 32], 32, 4, "bf16"),
