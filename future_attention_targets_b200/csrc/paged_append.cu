@@ -24,10 +24,13 @@ namespace kvpop {
 namespace cg = cooperative_groups;
 
 constexpr int kPaMaxSlice = 16384;     // keys one CTA holds at most (128 KiB); 8 x 16384 = the largest capacity
+// Place of key i: the 16 of a 128-byte line permuted by the line's number, so that threads that each read
+// consecutive keys meet different banks.
+__device__ __forceinline__ int placed(int i) { return i ^ ((i >> 4) & 15); }
 constexpr int append_threads(bool chunk) { return chunk ? 512 : 256; }
 constexpr int kPaBits = 11;           // of a digit
 constexpr int kPaBins = 1 << kPaBits;
-constexpr int kPaList = 2 * kPaBins * 4 / static_cast<int>(sizeof(RowEntry));   // as the two histograms
+constexpr int kPaList = kPaBins * 4 / static_cast<int>(sizeof(RowEntry));   // as the histogram
 constexpr uint64_t kStays = ~0ull;
 
 // Larger float -> larger key, never 2^32 - 1; -0 equals +0 (the addition makes it +0); NaN -> 0, below every number
@@ -90,8 +93,8 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
   extern __shared__ __align__(16) uint64_t keys[];       // kChunk: this CTA's slice; then the rows to write
   __shared__ Candidate best[kPaWarps + 1];               // one out: of each warp; [kPaWarps] = of the CTA
-  __shared__ __align__(16) uint32_t hist[kChunk ? 2 : 1][kChunk ? kPaBins : 4];   // a pass's histogram, read by the cluster
-  __shared__ __align__(16) uint32_t vary[2][4];          // AND and OR of a pass's keys, high and low halves
+  __shared__ __align__(16) uint32_t hist[kChunk ? kPaBins : 4];   // a pass's histogram, read by the cluster
+  __shared__ __align__(16) uint32_t vary[4];             // AND and OR of a pass's keys, high and low halves
   __shared__ uint64_t every_any[2];                      // the same of the whole cluster
   __shared__ uint32_t sel[3];
   __shared__ uint32_t ranks[3];                          // victims before this slice, victims in all, undecided before it
@@ -144,37 +147,6 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
     // Positions below sinks wrap to numbers from 2^31 - sinks up, which no span exceeds.
     const bool goes = static_cast<uint32_t>(pos) - static_cast<uint32_t>(p.sinks) < span;
     return goes ? (static_cast<uint64_t>(weight_key(w)) << 32) | static_cast<uint32_t>(0x7fffffff - pos) : kStays;
-  };
-  // Calls use(slot, keys) for the slots of this CTA's slice, 4 per thread and step (a page has at least 8 slots and
-  // slices are multiples of 8, so four slots share a page and an aligned 16 bytes).
-  auto for_keys = [&](auto&& use) {
-    for (int base = s0 + 4 * tid; base < s1; base += 4 * kPaThreads * kU) {
-      int page[kU];
-      float4 w[kU];
-      int4 x[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int s = base + u * 4 * kPaThreads;
-        page[u] = s < s1 ? page_of(p.c, b, s >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 1) : -1;
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int64_t at = meta_at(max(page[u], 0), (base + u * 4 * kPaThreads) & page_mask);
-        if (page[u] >= 0) {
-          w[u] = *reinterpret_cast<const float4*>(p.c.weight + at);
-          x[u] = *reinterpret_cast<const int4*>(p.c.pos + at);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int s = base + u * 4 * kPaThreads;
-        const float wf[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        const int xi[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (s + i < s1) use(s + i, page[u] >= 0 ? key_of(wf[i], xi[i]) : kStays);
-      }
-    }
   };
   // Token i of the sequence into `slot` (< 0: none for it), where position `old` goes (-1: nothing does).
   auto place = [&](int i, int slot, int old) {
@@ -271,9 +243,8 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
       p.c.seen[row] = seen + 1;
     }
   } else {
-    // Rows to write, up to kPaList at a time, where the histograms are at other times.
+    // Rows to write, up to kPaList at a time, where the histogram is at other times.
     RowEntry* list = reinterpret_cast<RowEntry*>(hist);
-    const uint32_t lanes_below = (1u << lane) - 1u;
     // Tokens for free slots: an even share for each CTA of the cluster.
     if (f > 0) {
       const int share = (f + ctas - 1) / ctas, f0 = min(f, cta * share), f1 = min(f, f0 + share);
@@ -286,36 +257,77 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
       }
     }
     if (e > 0) {
-      for_keys([&](int s, uint64_t k) { keys[s - s0] = k; });
       // Radix select, smallest first.  A key with (key & mask) < prefix is taken, one with == prefix is undecided.
-      // Each pass also finds which bits vary among the undecided keys, so that the next digit starts at the first one
-      // that does: weights that are all equal cost one pass, not three, before positions decide.
+      // Each pass counts a digit and also finds which bits vary among the undecided keys, so that the next digit
+      // starts at the first one that does: weights that are all equal cost one pass, not three, before positions
+      // decide.  The first pass counts while the keys arrive.
       uint64_t prefix = 0, mask = 0;
       uint32_t need = static_cast<uint32_t>(e);          // still to take among the undecided
       bool whole = false;                                // every undecided key is taken
       int top = 64;                                      // bits top .. 63 are decided
+      auto clear = [&] {
+        for (int i = tid; i < kPaBins / 4; i += kPaThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+        if (tid == 0) sel[2] = 0;
+        if (tid < 4) vary[tid] = tid < 2 ? ~0u : 0u;
+        __syncthreads();
+      };
+      // Counters that many keys share would serialise the lanes: one addition for those that agree with lane 0's key.
+      auto count = [&](bool in, uint32_t digit) {
+        const uint32_t first = __shfl_sync(0xffffffffu, digit, 0);
+        const uint32_t same = __ballot_sync(0xffffffffu, in && digit == first);
+        if (lane == 0 && same != 0) atomicAdd(&hist[first], static_cast<uint32_t>(__popc(same)));
+        if (in && digit != first) atomicAdd(&hist[digit], 1u);
+      };
+      uint64_t every = ~0ull, any = 0;                   // AND and OR of the undecided keys
+      clear();
+      for (int base = s0; base < s1; base += 4 * kPaThreads * kU) {
+        int page[kU];
+        float4 w[kU];
+        int4 x[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int s = base + 4 * (tid + u * kPaThreads);
+          page[u] = s < s1 ? page_of(p.c, b, s >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 1) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int64_t at = meta_at(max(page[u], 0), (base + 4 * (tid + u * kPaThreads)) & page_mask);
+          w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          x[u] = make_int4(-1, -1, -1, -1);              // a position that never goes
+          if (page[u] >= 0) {
+            w[u] = *reinterpret_cast<const float4*>(p.c.weight + at);
+            x[u] = *reinterpret_cast<const int4*>(p.c.pos + at);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int s = base + 4 * (tid + u * kPaThreads);
+          const float wf[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+          const int xi[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t k = s + i < s1 ? key_of(wf[i], xi[i]) : kStays;
+            const bool in = k != kStays;
+            if (s + i < s1) keys[placed(s + i - s0)] = k;
+            if (in) every &= k, any |= k;
+            count(in, static_cast<uint32_t>(k >> (64 - kPaBits)));
+          }
+        }
+      }
       for (int pass = 0; top > 0; ++pass) {
         const int bits = min(top, kPaBits), shift = top - bits;
-        uint32_t* mine = hist[pass & 1];
-        for (int i = tid; i < kPaBins / 4; i += kPaThreads) reinterpret_cast<uint4*>(mine)[i] = make_uint4(0, 0, 0, 0);
-        if (tid == 0) sel[2] = 0;
-        if (tid < 4) vary[pass & 1][tid] = tid < 2 ? ~0u : 0u;
-        __syncthreads();
-        uint64_t every = ~0ull, any = 0;                 // AND and OR of the undecided keys
-        for (int base = 0; base < s1 - s0; base += kPaThreads) {
-          const int i = base + tid;
-          const uint64_t k = i < s1 - s0 ? keys[i] : kStays;
-          const bool in = k != kStays && (k & mask) == prefix;
-          const uint32_t digit = static_cast<uint32_t>(k >> shift) & ((1u << bits) - 1);
-          const uint32_t votes = __ballot_sync(0xffffffffu, in);
-          if (votes == 0) continue;
-          if (in) every &= k, any |= k;
-          // Counters that many keys share would serialise the lanes: one addition where a warp's keys agree.
-          const int lead = __ffs(votes) - 1;
-          const uint32_t first = __shfl_sync(0xffffffffu, digit, lead);
-          const uint32_t same = __ballot_sync(0xffffffffu, in && digit == first);
-          if (lane == lead) atomicAdd(&mine[first], static_cast<uint32_t>(__popc(same)));
-          if (in && digit != first) atomicAdd(&mine[digit], 1u);
+        if (pass > 0) {
+          cluster.sync();      // every CTA has read this one's counters
+          clear();
+          every = ~0ull, any = 0;
+          for (int base = 0; base < s1 - s0; base += kPaThreads) {
+            const int i = base + tid;
+            const uint64_t k = i < s1 - s0 ? keys[placed(i)] : kStays;
+            const bool in = k != kStays && (k & mask) == prefix;
+            if (__ballot_sync(0xffffffffu, in) == 0) continue;
+            if (in) every &= k, any |= k;
+            count(in, static_cast<uint32_t>(k >> shift) & ((1u << bits) - 1));
+          }
         }
         {
           const uint32_t a1 = __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(every >> 32));
@@ -323,13 +335,13 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
           const uint32_t o1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32));
           const uint32_t o0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
           if (lane == 0) {
-            atomicAnd(&vary[pass & 1][0], a1);
-            atomicAnd(&vary[pass & 1][1], a0);
-            atomicOr(&vary[pass & 1][2], o1);
-            atomicOr(&vary[pass & 1][3], o0);
+            atomicAnd(&vary[0], a1);
+            atomicAnd(&vary[1], a0);
+            atomicOr(&vary[2], o1);
+            atomicOr(&vary[3], o0);
           }
         }
-        cluster.sync();        // a buffer is cleared again two passes on, past a barrier after its last reader
+        cluster.sync();
         constexpr int kPer = kPaBins / kPaThreads;       // consecutive counters of a thread
         static_assert(kPer == 4, "one 16-byte word of counters per thread");
         uint32_t c[kPer] = {}, all = 0;
@@ -339,14 +351,14 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             x[i] = make_uint4(0, 0, 0, 0);
-            if (q0 + i < ctas) x[i] = reinterpret_cast<const uint4*>(cluster.map_shared_rank(mine, q0 + i))[tid];
+            if (q0 + i < ctas) x[i] = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, q0 + i))[tid];
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) c[0] += x[i].x, c[1] += x[i].y, c[2] += x[i].z, c[3] += x[i].w;
         }
         if (warp == 0) {
           uint4 v = make_uint4(~0u, ~0u, 0u, 0u);
-          if (lane < ctas) v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(vary[pass & 1], lane));
+          if (lane < ctas) v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(vary, lane));
           v.x = __reduce_and_sync(0xffffffffu, v.x), v.y = __reduce_and_sync(0xffffffffu, v.y);
           v.z = __reduce_or_sync(0xffffffffu, v.z), v.w = __reduce_or_sync(0xffffffffu, v.w);
           if (lane == 0) every_any[0] = (static_cast<uint64_t>(v.x) << 32) | v.y, every_any[1] = (static_cast<uint64_t>(v.z) << 32) | v.w;
@@ -399,24 +411,28 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
         __syncthreads();                                 // the shared words of this pass are read
       }
       // Victims of this slice: those below the prefix, and of the undecided all or (equal keys, which need equal
-      // positions) the first `need` in slot order.  A warp looks at `per` steps of 32 consecutive slots, so that
-      // slot order is warp, step, lane; a thread remembers what it saw in a bit per step.
+      // positions) the first `need` in slot order.  A thread looks at `per` consecutive slots and remembers what it
+      // saw in a bit each.
       const int per = (p.slice + kPaThreads - 1) / kPaThreads;         // <= 32
-      const int i0 = warp * per * 32 + lane;
+      const int i0 = tid * per;
       uint32_t below_bits = 0, equal_bits = 0;
-      for (int j = 0; j < per; ++j) {
-        const int i = i0 + 32 * j;
-        const uint64_t k = i < s1 - s0 ? keys[i] : kStays;
+      for (int j = 0; j < per && i0 + j < s1 - s0; ++j) {
+        const uint64_t k = keys[placed(i0 + j)];
         const uint64_t head = k & mask;
         below_bits |= static_cast<uint32_t>(k != kStays && (head < prefix || (whole && head == prefix))) << j;
         equal_bits |= static_cast<uint32_t>(k != kStays && !whole && head == prefix) << j;
       }
-      // Exclusive scan over the warps, and the totals for the cluster.
-      const uint32_t below_w = __reduce_add_sync(0xffffffffu, __popc(below_bits));
-      const uint32_t equal_w = __reduce_add_sync(0xffffffffu, __popc(equal_bits));
-      if (lane == 0) warp_sum[warp] = below_w | (equal_w << 16);       // at most 1,024 each
+      // Exclusive scans over the block, below and equal in a word (at most 1,024 of each in a warp), and the totals.
+      const uint32_t own = __popc(below_bits) | (__popc(equal_bits) << 16);
+      uint32_t both = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, both, o);
+        if (lane >= o) both += y;
+      }
+      if (lane == 31) warp_sum[warp] = both;
       __syncthreads();
-      uint32_t below = 0, equal = 0, below_all = 0, equal_all = 0;
+      uint32_t below = (both - own) & 0xffffu, equal = (both - own) >> 16, below_all = 0, equal_all = 0;
 #pragma unroll
       for (int w = 0; w < kPaWarps; ++w) {
         const uint32_t x = warp_sum[w];
@@ -453,28 +469,19 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
       const uint32_t rank0 = ranks[0], all_taken = ranks[1], seen_equal = ranks[2];
       const uint32_t left = need > seen_equal ? need - seen_equal : 0u;     // undecided ones that this slice gives
       uint32_t goes = below_bits;
-      if (!whole) {
+      if (equal_bits != 0) {
         uint32_t eq_rank = equal;
-        for (int j = 0; j < per; ++j) {
-          const uint32_t votes = __ballot_sync(0xffffffffu, (equal_bits >> j) & 1u);
-          if (((equal_bits >> j) & 1u) && eq_rank + __popc(votes & lanes_below) < left) goes |= 1u << j;
-          eq_rank += __popc(votes);
-        }
+        for (uint32_t bits = equal_bits; bits != 0; bits &= bits - 1, ++eq_rank)
+          if (eq_rank < left) goes |= bits & (0u - bits);
       }
       const int here = static_cast<int>(below_all + min(equal_all, left));
-      const uint32_t first = below + min(equal, left);                      // rank of this warp's first victim
+      const uint32_t first = below + min(equal, left);                      // rank of this thread's first victim
       for (int done = 0; done < here; done += kPaList) {
         // Slots and positions in slot order, then a row entry for each.
-        uint32_t rank = first - static_cast<uint32_t>(done);                // wraps: outside the list
-        for (int j = 0; j < per; ++j) {
-          const bool go = (goes >> j) & 1u;
-          const uint32_t votes = __ballot_sync(0xffffffffu, go);
-          const uint32_t at = rank + __popc(votes & lanes_below);
-          if (go && at < kPaList) {
-            const int i = i0 + 32 * j;
-            list[at] = {s0 + i, 0x7fffffffu - static_cast<uint32_t>(keys[i])};
-          }
-          rank += __popc(votes);
+        uint32_t at = first - static_cast<uint32_t>(done);                  // wraps: outside the list
+        for (uint32_t bits = goes; bits != 0; bits &= bits - 1, ++at) {
+          const int i = i0 + __ffs(bits) - 1;
+          if (at < kPaList) list[at] = {s0 + i, 0x7fffffffu - static_cast<uint32_t>(keys[placed(i)])};
         }
         __syncthreads();
         const int entries = min(here - done, kPaList);
@@ -501,7 +508,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
 // it looks at one step's weights and positions, the next one's, and the page
 // numbers, counts and new rows of the one after that, are on their way into
 // shared memory, so the SM always has bytes in flight and no load is waited for
-// (256 x 8 rows of 4,032 slots: 23.9 us with a CTA per row, STREAM_MEASURED).
+// (256 x 8 rows of 4,032 slots: 23.9 us with a CTA per row, 19.5 so).
 // A thread reads what it copied itself; the barrier of a row's end shows warp 0
 // the rest.
 constexpr int kPsThreads = 256;
@@ -672,10 +679,11 @@ constexpr int kPsRows = 3 * 148;     // more rows than this are streamed
 
 // CTAs per row.  One out: the largest of 8, 4, 2, 1 whose clusters leave two
 // CTAs per SM at most and 1,024 slots per CTA at least.  Several out: the
-// fewest that leave slices of 8,192 slots at most, and more while the CTAs do
-// not fill the SMs and slices are over 2,048 slots: every pass of the select
-// is a barrier of the cluster (24 x 8 rows of 16,000 slots: AC8 us with 8
-// CTAs of 256 threads per row, AC2 us with 2 of 512).
+// fewest that leave slices of 8,192 slots at most, and more while half the
+// SMs would have no CTA and slices are over 2,048 slots: every pass of the
+// select is a barrier of the cluster, and larger clusters wait for room
+// (24 x 8 rows of 16,000 slots: 47, 41, 56 and 121 us with 1, 2, 4 and 8 CTAs
+// per row; 4 x 8 rows: 35, 23 and 33 us with 1, 4 and 8).
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const bool chunk = !p.one_each;
@@ -693,13 +701,13 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
   }
   int ctas = 1;
   if (chunk) {
-    while (ctas < 8 && (p.c.capacity > 8192 * ctas || (rows * ctas < 148 && p.c.capacity > 2048 * ctas))) ctas <<= 1;
+    while (ctas < 8 && (p.c.capacity > 8192 * ctas || (rows * ctas <= 74 && p.c.capacity > 2048 * ctas))) ctas <<= 1;
   } else {
     ctas = 8;
     while (ctas > 1 && (rows * ctas > 2 * 148 || p.c.capacity < 1024 * ctas)) ctas >>= 1;
   }
   p.slice = ((p.c.capacity + ctas - 1) / ctas + 7) / 8 * 8;
-  const size_t smem = chunk ? static_cast<size_t>(p.slice) * 8 : 0;
+  const size_t smem = chunk ? static_cast<size_t>(p.slice + 15) / 16 * 128 : 0;
   const dim3 grid(static_cast<unsigned>(rows * ctas)), block(append_threads(chunk));
   static std::atomic<uint64_t> ready[4];
   auto go = [&](auto kern, int which) {

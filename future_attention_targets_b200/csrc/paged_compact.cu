@@ -39,7 +39,7 @@ __device__ __forceinline__ int block_sum_scan(int x, int* sums, int* total) {
 }
 
 template <int D, bool kF8>
-__global__ void __launch_bounds__(kPcThreads, 4) paged_compact_kernel(const __grid_constant__ PagedCompactParams p) {
+__global__ void __launch_bounds__(kPcThreads, kF8 ? 5 : 4) paged_compact_kernel(const __grid_constant__ PagedCompactParams p) {
   __shared__ int sums[kPcWarps];
   __shared__ RowEntry list[kPcMaxBlock];
   const int tid = threadIdx.x;
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kPcThreads, 4) paged_compact_kernel(const __gr
     const uint4* v = reinterpret_cast<const uint4*>(mask + head);
     // Non-zero bytes: bit 7 of ((x & 0x7f) + 0x7f) | x, which cannot carry into the next byte.
     auto bits = [](uint32_t x) { return __popc((((x & 0x7f7f7f7fu) + 0x7f7f7f7fu) | x) & 0x80808080u); };
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < words; i += kPcThreads) {
       const uint4 x = __ldg(v + i);
       c += bits(x.x) + bits(x.y) + bits(x.z) + bits(x.w);
@@ -106,9 +106,10 @@ __global__ void __launch_bounds__(kPcThreads, 4) paged_compact_kernel(const __gr
 cudaError_t launch_paged_compact(PagedCompactParams& p, int head_dim, bool f8, cudaStream_t stream) {
   int longest = 1;
   for (int b = 0; b < p.c.batch; ++b) longest = std::max(longest, p.start[b + 1] - p.start[b]);
-  // 256 positions per CTA keep the CTAs many and even (8 prompts of 100,003 tokens in all: PK256 us, with 1,024 PK1024);
-  // beyond 32,768 tokens counting the mask again 4 times as often would show.
-  p.block = longest <= 32768 ? 256 : kPcMaxBlock;
+  // Short blocks keep the CTAs many and even; the conversion to e4m3 has more to do per row and takes 512 positions
+  // (8 prompts of 100,003 tokens in all, e4m3: 80 us with 512, 82 with 256; bf16: 85 and 83.5, 99% of the copy
+  // bandwidth).  Beyond 32,768 tokens counting the mask again 4 times as often would show.
+  p.block = longest > 32768 ? kPcMaxBlock : f8 ? 512 : 256;
   const dim3 grid(p.c.batch * p.c.n_kv_heads, (longest + p.block - 1) / p.block), block(kPcThreads);
   if (head_dim == 128)
     return f8 ? launch_paged(paged_compact_kernel<128, true>, grid, block, 0, 1, stream, p)
