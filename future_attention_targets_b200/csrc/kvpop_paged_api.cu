@@ -167,7 +167,7 @@ kvpop_status kvpop_paged_compact_kv(const void* k, const void* v, const uint8_t*
                                     int32_t* dev_status, void* stream) {
   Range range(__func__);
   kvpop_status st;
-  if (k == nullptr || v == nullptr) return fail(KVPOP_ERR_INVALID_ARG, "k or v is NULL");
+  if ((k == nullptr || v == nullptr) && total_tokens != 0) return fail(KVPOP_ERR_INVALID_ARG, "k or v is NULL");
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(KVPOP_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
   if (cu_seqlens == nullptr) return fail(KVPOP_ERR_INVALID_ARG, "cu_seqlens is NULL");
   if ((st = check_cache(cache)) != KVPOP_OK) return st;

@@ -62,6 +62,7 @@ __device__ __forceinline__ void write_one(const PagedAppendParams& p, int b, int
   const int lane = threadIdx.x & 31;
   const int off = slot & ((1 << p.c.page_shift) - 1);
   int page = -1;
+  KVPOP_CHECK(slot < p.c.capacity && b < p.c.batch && h < p.c.n_kv_heads, p.dbg, DBG_PAGED_APPEND, 7);
   if (slot < 0) debug_fail(p.status, DBG_PAGED_APPEND, 3);
   else page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 2);
   if (lane == 0 && p.evicted != nullptr) p.evicted[static_cast<int64_t>(tok) * p.c.n_kv_heads + h] = page >= 0 ? old : -2;
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   // Token i of the sequence into `slot` (< 0: none for it), where position `old` goes (-1: nothing does).
   auto place = [&](int i, int slot, int old) {
     int page = -1, off = 0;
+    KVPOP_CHECK(i >= 0 && i < m && slot < cap, p.dbg, DBG_PAGED_APPEND, 6);
     if (slot >= 0) {
       page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_APPEND, 2);
       off = slot & page_mask;
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
           for (int i = 0; i < 4; ++i) {
             const uint64_t k = s + i < s1 ? key_of(wf[i], xi[i]) : kStays;
             const bool in = k != kStays;
-            if (s + i < s1) keys[placed(s + i - s0)] = k;
+            if (s + i < s1 && KVPOP_IN(s + i - s0 < p.slice, p.dbg, DBG_PAGED_APPEND, 4)) keys[placed(s + i - s0)] = k;
             if (in) every &= k, any |= k;
             count(in, static_cast<uint32_t>(k >> (64 - kPaBits)));
           }
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
         uint32_t at = first - static_cast<uint32_t>(done);                  // wraps: outside the list
         for (uint32_t bits = goes; bits != 0; bits &= bits - 1, ++at) {
           const int i = i0 + __ffs(bits) - 1;
-          if (at < kPaList) list[at] = {s0 + i, 0x7fffffffu - static_cast<uint32_t>(keys[placed(i)])};
+          if (at < kPaList && KVPOP_IN(s0 + i < n, p.dbg, DBG_PAGED_APPEND, 5)) list[at] = {s0 + i, 0x7fffffffu - static_cast<uint32_t>(keys[placed(i)])};
         }
         __syncthreads();
         const int entries = min(here - done, kPaList);

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kPcThreads, kF8 ? 5 : 4) paged_compact_kernel(
   const int n = min(total, max(0, p.c.capacity - before));
   for (int i = 0; i < per; ++i) {
     if (!((kept >> i) & 1u)) continue;
-    if (rank < n) {
+    if (rank < n && KVPOP_IN(rank >= 0 && rank < kPcMaxBlock && before + rank < p.c.capacity && s0 + first + i < p.total_tokens,
+                             p.dbg, DBG_PAGED_COMPACT, 2)) {
       const int slot = before + rank, off = slot & ((1 << p.c.page_shift) - 1);
       const int page = page_of(p.c, b, slot >> p.c.page_shift, p.status, DBG_PAGED_COMPACT, 1);
       list[rank] = row_entry(page, off, first + i);

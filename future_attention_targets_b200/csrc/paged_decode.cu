@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
   if (threadIdx.x == 0) bad_pages = 0;
   __syncthreads();
   grid_wait();
+  grid_launch_next();                       // the next kernel's CTAs come in as these leave, and wait for the last
 
   const bool held = items <= kPdItemsHeld && !p.whole;
   auto slots_of = [&](int i) { return held ? slots_held[i] : item_slots(p, i); };
@@ -355,6 +356,8 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
   // Page of slot lo + at.
   auto page_at = [&](int at) {
     const int chunk = at / kPdChunk;
+    if (!KVPOP_IN(at >= 0 && at < cnt && ((lo + at) >> shift) - entry0(chunk) <= kPdChunk / kPdMinPage, p.dbg, DBG_PAGED_DECODE, 2))
+      return -1;
     return pages[chunk & 1][((lo + at) >> shift) - entry0(chunk)];
   };
   // Starts the copies of rows kFirst .. kFirst + kN - 1 of a tile, which lie on one page from slot lo + at on.  They
@@ -364,6 +367,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
     const int page = page_at(at);
     if (page < 0) return;                                 // stays as it is in the ring
     const int off = (lo + at) & page_mask;
+    KVPOP_CHECK(off + kN <= page_mask + 1, p.dbg, DBG_PAGED_DECODE, 3);
     const uint8_t* kp = kb + static_cast<uint64_t>(static_cast<uint32_t>(page)) * k_page + static_cast<uint64_t>(off) * k_slot;
     const uint8_t* vp = vb + static_cast<uint64_t>(static_cast<uint32_t>(page)) * v_page + static_cast<uint64_t>(off) * v_slot;
 #pragma unroll
@@ -456,7 +460,8 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
       float y = -INFINITY;
 #pragma unroll
       for (int half = 0; half < T::kH; ++half) y = fmaxf(y, fmaxf(s[half][2 * r], s[half][2 * r + 1]));
-      if (p.scores != nullptr && g + 8 * r < G) {
+      if (p.scores != nullptr && g + 8 * r < G &&
+          KVPOP_IN(lo + (tile + 1) * T::kSlots <= p.score_pitch, p.dbg, DBG_PAGED_DECODE, 4)) {
         float* to = p.scores + (bg0 + g + 8 * r) * p.score_pitch + lo + tile * T::kSlots + 2 * t;
 #pragma unroll
         for (int half = 0; half < T::kH; ++half)
@@ -571,7 +576,6 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
     }
   }
   copy_wait<0>();
-  if (x >= x1) grid_launch_next();
   __syncthreads();                                        // the rings are free
 
   // Join the warps: every lane holds part of its rows' sums, all four lanes of a row the same maximum.
@@ -602,6 +606,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
   const float vs = kF8 && p.c.v_scale != nullptr ? p.c.v_scale[h] : 1.f;
   const bool all = cnt == n;                              // the whole item: the result; else a part of it
   const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (lo == 0 ? 1 : 0)) * 16;
+  KVPOP_CHECK(lo + cnt <= n && n <= p.c.capacity && row < p.c.batch * p.c.n_kv_heads, p.dbg, DBG_PAGED_DECODE, 5);
   if (threadIdx.x < G) {
     const int i = threadIdx.x;
     float top = -INFINITY, sum = 0.f;
@@ -727,7 +732,10 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
   }
   // Parts of head i's item: of CTAs x .. x + y - 1, the first in place 1.
   auto parts_of = [&](int i) { return p.item_parts[row * p.head_chunks + i / 16]; };
-  auto part_at = [&](const int2& q, int i, int j) { return (static_cast<int64_t>(q.x + j) * 2 + (j == 0 ? 1 : 0)) * 16 + i % 16; };
+  auto part_at = [&](const int2& q, int i, int j) {
+    KVPOP_CHECK(q.x >= 0 && j < q.y && q.x + j < p.ctas, p.dbg, DBG_PAGED_JOIN, 1);
+    return (static_cast<int64_t>(q.x + j) * 2 + (j == 0 ? 1 : 0)) * 16 + i % 16;
+  };
   for (int i = warp; i < p.group; i += kPjWarps) {
     const int2 q = parts_of(i);
     float l2 = INFINITY;
@@ -847,10 +855,10 @@ static cudaError_t launch_decode_of(const PagedDecodeParams& p, cudaStream_t str
   };
   const cudaError_t e = p.group > 8 ? go(paged_decode_kernel<D, kF8, true>, 1) : go(paged_decode_kernel<D, kF8, false>, 0);
   if (e != cudaSuccess || p.whole) return e;
-  // Join: a CTA per row where that is a wave, else up to one per kPjSlots slots (or per head, without weights).
+  // Join: six CTAs per SM or more where rows are few, up to one per kPjSlots slots (or per head, without weights).
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const int most = p.scores != nullptr ? (p.c.capacity + kPjSlots - 1) / kPjSlots : std::min(p.group, 16);
-  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * 4 / rows)));
+  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (148 * 6 + rows - 1) / rows)));
   return launch_paged(paged_join_kernel<D>, dim3(static_cast<unsigned>(rows), parts), dim3(kPjThreads), 0, 1, stream, p);
 }
 

@@ -30,7 +30,9 @@
  * no part (attention), are left unwritten (compaction, append) and are not
  * evicted (append), and *dev_status, if given and still 0, receives
  * KVPOP_ERR_BOUNDS | site << 8 | kernel << 16 for kvpop_check_device_status.
- * A page may not appear twice among the rows that one call writes.
+ * A page may not appear twice among the rows that one call writes (the weights
+ * count as written by an attention that accumulates); rows that are only read
+ * may share pages, such as those of a common prefix.  Positions stay below 2^31.
  */
 #ifndef KVPOP_PAGED_H_
 #define KVPOP_PAGED_H_
@@ -76,7 +78,7 @@ typedef struct {
  * rest are dropped.  pos, count (slots used) and seen (the sequence's length)
  * are written, and weight = score (the attention a token has received so far:
  * kvpop_future_target with window 0 gives exactly that for a prompt) or 0.
- *   k, v         bf16 [T, n_kv_heads, head_dim], 16-byte aligned
+ *   k, v         bf16 [T, n_kv_heads, head_dim], 16-byte aligned (NULL with T = 0)
  *   keep         uint8 [n_kv_heads, T], or NULL to keep every position
  *   score        fp32 [n_kv_heads, T], or NULL for 0 (needs cache->weight_pages otherwise)
  *   cu_seqlens   HOST int32 [batch + 1]; batch = cache->batch at most 512; cu_seqlens[batch] = total_tokens
@@ -103,10 +105,9 @@ KVPOP_API kvpop_status kvpop_paged_compact_kv(const void* k, const void* v, cons
  *                  free slot, -2 where it was not stored
  * Rows with count < 0 are left as they are.  A token without a slot (which
  * needs a bad page, or positions that break the rules above) is not stored
- * and reported in *dev_status.  One row is handled by a cluster of up to 8
- * CTAs; the radix select is exact, no atomics touch results, and nothing but
- * counts and positions on the device decides, so the call can be captured in
- * a graph and replayed. */
+ * and reported in *dev_status.  The choice is exact and depends on no order of
+ * execution.  Nothing but counts, positions and weights on the device decides,
+ * so the call can be captured in a graph and replayed. */
 KVPOP_API kvpop_status kvpop_paged_append_kv(const void* k_new, const void* v_new, int64_t token_stride,
                                              const int32_t* cu_new, const kvpop_paged_cache* cache, int32_t window,
                                              int32_t sinks, int32_t* evicted, int32_t* dev_status, void* stream);

@@ -142,7 +142,8 @@ def quantise(x, pool_dtype, scale):
     if pool_dtype != E4M3:
         return x
     # The fp32 quotient is IEEE in numpy; clip keeps NaN.
-    y = np.clip((x.float().numpy() / np.float32(scale)).astype(np.float32), -448, 448)
+    with np.errstate(all="ignore"):
+        y = np.clip((x.float().numpy() / np.float32(scale)).astype(np.float32), -448, 448)
     return torch.from_numpy(y).to(E4M3)
 
 
