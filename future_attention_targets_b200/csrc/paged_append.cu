@@ -16,6 +16,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvpop_paged.cuh"
 
@@ -27,7 +28,6 @@ constexpr int kPaMaxSlice = 16384;     // keys one CTA holds at most (128 KiB); 
 // Place of key i: the 16 of a 128-byte line permuted by the line's number, so that threads that each read
 // consecutive keys meet different banks.
 __device__ __forceinline__ int placed(int i) { return i ^ ((i >> 4) & 15); }
-constexpr int append_threads(bool chunk) { return chunk ? 512 : 256; }
 constexpr int kPaBits = 11;           // of a digit
 constexpr int kPaBins = 1 << kPaBits;
 constexpr int kPaList = kPaBins * 4 / static_cast<int>(sizeof(RowEntry));   // as the histogram
@@ -86,10 +86,9 @@ __device__ __forceinline__ void write_one(const PagedAppendParams& p, int b, int
   }
 }
 
-template <int D, bool kF8, bool kChunk>
-__global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
-    paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
-  constexpr int kPaThreads = append_threads(kChunk), kPaWarps = kPaThreads / 32;
+template <int D, bool kF8, bool kChunk, int kPaThreads>
+__global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+  constexpr int kPaWarps = kPaThreads / 32;
   cg::cluster_group cluster = cg::this_cluster();
   const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
   extern __shared__ __align__(16) uint64_t keys[];       // kChunk: this CTA's slice; then the rows to write
@@ -102,6 +101,11 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
   __shared__ uint32_t taken_here[2];                     // kChunk: victims and undecided in this slice, read by the cluster
   __shared__ uint32_t warp_sum[kPaWarps];
 
+  // A barrier of the row's CTAs.
+  auto sync_row = [&] {
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / ctas, b = row / p.c.n_kv_heads, h = row - b * p.c.n_kv_heads;
   const int page_mask = (1 << p.c.page_shift) - 1;
@@ -235,8 +239,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
       old = c.pos;
     }
     // Warp 0 of CTA 0 has the slot; every CTA's count and candidate has been read.
-    if (ctas > 1) cluster.sync();
-    else __syncthreads();
+    sync_row();
     if (cta != 0) return;
     if (warp > 0) return;
     write_one<D, kF8>(p, b, h, tok0, slot, old, seen, fresh);
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
       for (int pass = 0; top > 0; ++pass) {
         const int bits = min(top, kPaBits), shift = top - bits;
         if (pass > 0) {
-          cluster.sync();      // every CTA has read this one's counters
+          sync_row();      // every CTA has read this one's counters
           clear();
           every = ~0ull, any = 0;
           for (int base = 0; base < s1 - s0; base += kPaThreads) {
@@ -343,20 +346,28 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
             atomicOr(&vary[3], o0);
           }
         }
-        cluster.sync();
+        sync_row();
         constexpr int kPer = kPaBins / kPaThreads;       // consecutive counters of a thread
-        static_assert(kPer == 4, "one 16-byte word of counters per thread");
         uint32_t c[kPer] = {}, all = 0;
 #pragma unroll
-        for (int q0 = 0; q0 < 8; q0 += 4) {              // four peers' words on their way at a time
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (q0 + i < ctas) x[i] = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, q0 + i))[tid];
+        for (int j = 0; j < kPer / 4; ++j) {
+          const int at = tid * (kPer / 4) + j;
+          if (ctas == 1) {
+            const uint4 x = reinterpret_cast<const uint4*>(hist)[at];
+            c[4 * j] = x.x, c[4 * j + 1] = x.y, c[4 * j + 2] = x.z, c[4 * j + 3] = x.w;
+            continue;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[0] += x[i].x, c[1] += x[i].y, c[2] += x[i].z, c[3] += x[i].w;
+          for (int q0 = 0; q0 < 8; q0 += 4) {            // four peers' words on their way at a time
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = make_uint4(0, 0, 0, 0);
+              if (q0 + i < ctas) x[i] = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, q0 + i))[at];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[4 * j] += x[i].x, c[4 * j + 1] += x[i].y, c[4 * j + 2] += x[i].z, c[4 * j + 3] += x[i].w;
+          }
         }
         if (warp == 0) {
           uint4 v = make_uint4(~0u, ~0u, 0u, 0u);
@@ -415,7 +426,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
       // Victims of this slice: those below the prefix, and of the undecided all or (equal keys, which need equal
       // positions) the first `need` in slot order.  A thread looks at `per` consecutive slots and remembers what it
       // saw in a bit each.
-      const int per = (p.slice + kPaThreads - 1) / kPaThreads;         // <= 32
+      const int per = (p.slice + kPaThreads - 1) / kPaThreads;         // <= 32: the host gives long slices 512 threads
       const int i0 = tid * per;
       uint32_t below_bits = 0, equal_bits = 0;
       for (int j = 0; j < per && i0 + j < s1 - s0; ++j) {
@@ -442,7 +453,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
         if (w < warp) below += x & 0xffffu, equal += x >> 16;
       }
       if (tid == 0) taken_here[0] = below_all, taken_here[1] = equal_all;
-      cluster.sync();
+      sync_row();
       if (warp == 0) {
         // Lane q holds slice q's counts; undecided keys are taken in slice order until `need` are.
         uint32_t bel = 0, eq = 0;
@@ -497,7 +508,7 @@ __global__ void __launch_bounds__(append_threads(kChunk), kChunk ? 2 : 4)
       if (cta == 0)
         for (int i = f + static_cast<int>(all_taken) + tid; i < m; i += kPaThreads) place(i, -1, -2);
     }
-    cluster.sync();                                      // the cluster has read counts, histograms and sums
+    sync_row();                                      // the cluster has read counts, histograms and sums
     if (cta == 0 && tid == 0) {
       p.c.count[row] = min(n + m, cap);
       p.c.seen[row] = seen + m;
@@ -709,9 +720,12 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
     while (ctas > 1 && (rows * ctas > 2 * 148 || p.c.capacity < 1024 * ctas)) ctas >>= 1;
   }
   p.slice = ((p.c.capacity + ctas - 1) / ctas + 7) / 8 * 8;
+  // Many short slices take 256 threads, so that four CTAs share an SM (200 x 8 rows of 1,000 slots: 70 us, with 512
+  // threads 87; 8 rows of 16,000 slots: 15 and 13).
+  const bool small = !chunk || (p.slice <= 2048 && rows * ctas > 2 * 148);
   const size_t smem = chunk ? static_cast<size_t>(p.slice + 15) / 16 * 128 : 0;
-  const dim3 grid(static_cast<unsigned>(rows * ctas)), block(append_threads(chunk));
-  static std::atomic<uint64_t> ready[4];
+  const dim3 grid(static_cast<unsigned>(rows * ctas)), block(small ? 256 : 512);
+  static std::atomic<uint64_t> ready[8];
   auto go = [&](auto kern, int which) {
     if (smem > 0) {
       const cudaError_t e = allow_smem(kern, kPaMaxSlice * 8, ready[which]);
@@ -719,12 +733,16 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
     }
     return launch_paged(kern, grid, block, smem, ctas, stream, p);
   };
-  if (head_dim == 128) {
-    if (f8) return chunk ? go(paged_append_kernel<128, true, true>, 0) : go(paged_append_kernel<128, true, false>, 0);
-    return chunk ? go(paged_append_kernel<128, false, true>, 1) : go(paged_append_kernel<128, false, false>, 1);
-  }
-  if (f8) return chunk ? go(paged_append_kernel<64, true, true>, 2) : go(paged_append_kernel<64, true, false>, 2);
-  return chunk ? go(paged_append_kernel<64, false, true>, 3) : go(paged_append_kernel<64, false, false>, 3);
+  auto of = [&](auto dim, auto eight, int which) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool kF8 = decltype(eight)::value;
+    if (!chunk) return go(paged_append_kernel<D, kF8, false, 256>, which);
+    return small ? go(paged_append_kernel<D, kF8, true, 256>, which) : go(paged_append_kernel<D, kF8, true, 512>, which + 1);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (head_dim == 128) return f8 ? of(D128(), std::true_type(), 0) : of(D128(), std::false_type(), 2);
+  return f8 ? of(D64(), std::true_type(), 4) : of(D64(), std::false_type(), 6);
 }
 
 }  // namespace kvpop

@@ -144,6 +144,11 @@ struct Tile {
   // chain of a step is then hidden by more warps (96 x 4 e4m3 rows of 8,192 slots, no weights: 178 -> 161 us).
   static constexpr int kStages = kRow == 64 ? 4 : kRow == 128 ? 2 : 3;
   static constexpr int ctas(bool wide) { return wide || kRow == 256 ? 2 : 3; }
+  // Whether a CTA adds the weights of long rows that it does whole, rather than the second kernel (256 x 8 rows of
+  // 4,032 slots: 690 us against 720; short rows are left to the second kernel's many warps: 256 x 8 rows of 1 to 4,032
+  // slots 107 against 117).  With three CTAs per SM its registers would spill in the attention loop (256 x 8 e4m3
+  // rows: 496 against 392).
+  static constexpr bool kSums = kRow == 256;
   static constexpr int kRing = kStages * kBytes;                // bytes of a warp's ring
 };
 
@@ -161,6 +166,7 @@ __device__ __forceinline__ int swizzle(int r) { return (r & 6) ^ ((r & 1) << 2);
 // Every CTA finds its share from the counts.
 constexpr int kPdBlock = 128;
 constexpr int kPdItem = 2;
+constexpr int kPdSumSlots = 1024;           // a whole row's weights are added by its CTA from this many slots on
 constexpr int kPdItemsHeld = 1024;          // items whose sizes a CTA keeps at hand
 
 __device__ __forceinline__ int item_slots(const PagedDecodeParams& p, int item) {
@@ -649,40 +655,61 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
       *reinterpret_cast<float4*>(p.part_o + (part + i) * D + d) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
     }
   }
-  // A whole item of a call without the second kernel: weight[c] += sum over its heads of 2^(s - lse2), four slots (of
-  // one page) per thread, from the scores that this CTA wrote.
-  if (p.whole && p.scores != nullptr) {
-    for (int at = 4 * threadIdx.x; at < n; at += 4 * kPdThreads) {
-      const int page = page_at(at);
-      if (page < 0) continue;
-      float* to = p.c.weight + ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << shift) + (at & page_mask);
-      const float* from = p.scores + bg0 * p.score_pitch + at;
-      const float4 w = *reinterpret_cast<const float4*>(to);
-      float add[4] = {0.f, 0.f, 0.f, 0.f};
+  if (all && p.scores != nullptr && p.head_chunks == 1 && (p.whole || (T::kSums && n >= kPdSumSlots))) {
+    constexpr int kU = T::kSums ? 2 : 1;
+    const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
+    for (int at0 = 4 * threadIdx.x; at0 < n; at0 += 4 * kU * kPdThreads) {
+      float4 w[kU];
+      float add[kU][4] = {};
+      float* to[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int at = at0 + u * 4 * kPdThreads;
+        const int page = at < n ? table[at >> shift] : -1;
+        const bool good = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.c.n_pages);
+        to[u] = good ? p.c.weight + ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << shift) + (at & page_mask) : nullptr;
+      }
 #pragma unroll
       for (int i0 = 0; i0 < kRows; i0 += 8) {
-        float4 s[8];
+        float4 s[kU][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < G) s[i] = *reinterpret_cast<const float4*>(from + (i0 + i) * static_cast<int64_t>(p.score_pitch));
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < G) {
-            const float z = fin[i0 + i].y;
-            add[0] += ex2(s[i].x - z), add[1] += ex2(s[i].y - z), add[2] += ex2(s[i].z - z), add[3] += ex2(s[i].w - z);
-          }
+          for (int i = 0; i < 8; ++i)
+            if (i0 + i < G && at0 + u * 4 * kPdThreads < n)
+              s[u][i] = __ldcg(reinterpret_cast<const float4*>(p.scores + (bg0 + i0 + i) * p.score_pitch + at0 + u * 4 * kPdThreads));
+        if (i0 == 0)
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            if (to[u] != nullptr) w[u] = *reinterpret_cast<const float4*>(to[u]);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i0 + i < G) {
+              const float z = fin[i0 + i].y;
+              add[u][0] += ex2(s[u][i].x - z), add[u][1] += ex2(s[u][i].y - z);
+              add[u][2] += ex2(s[u][i].z - z), add[u][3] += ex2(s[u][i].w - z);
+            }
       }
-      if (at + 3 < n) {
-        *reinterpret_cast<float4*>(to) = make_float4(w.x + add[0], w.y + add[1], w.z + add[2], w.w + add[3]);
-      } else {
-        const float old[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (at + e < n) to[e] = old[e] + add[e];
+      for (int u = 0; u < kU; ++u) {
+        if (to[u] == nullptr) continue;
+        const int at = at0 + u * 4 * kPdThreads;
+        if (at + 3 < n) {
+          *reinterpret_cast<float4*>(to[u]) =
+              make_float4(w[u].x + add[u][0], w[u].y + add[u][1], w[u].z + add[u][2], w[u].w + add[u][3]);
+        } else {
+          const float old[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            if (at + e < n) to[u][e] = old[e] + add[u][e];
+        }
       }
     }
   }
-  if (threadIdx.x == 0) bad_pages = 0;                    // read by all before the last barrier
+  __syncthreads();                                        // bad_pages is set no more
+  if (threadIdx.x == 0) bad_pages = 0;
   __syncthreads();                                        // before the next item's pages, rings and factors
   }
 }
@@ -702,7 +729,7 @@ constexpr int kPjSlots = 4 * kPjThreads;
 constexpr int kPjMaxGroup = 1024;
 constexpr int kPjHeads = 4;                                // heads whose scores are asked for together
 
-template <int D>
+template <int D, bool kSums>
 __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
   constexpr int kWords = D / 4;                            // 16-byte words of a part's row
   constexpr int kParts = kPjThreads / kWords;              // splits read side by side when there are many
@@ -730,6 +757,10 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
     if (at < p.c.capacity) page = table[at >> p.c.page_shift];
     ask(at, 0);
   }
+  // A row that one CTA did whole is done with, but for its weights if that does not add them.
+  const bool one = p.head_chunks == 1 && p.item_parts[row].y == 1;
+  if (one && (p.scores == nullptr || (kSums && min(count, p.c.capacity) >= kPdSumSlots))) return;
+  const bool done = p.scores == nullptr;
   // Parts of head i's item: of CTAs x .. x + y - 1, the first in place 1.
   auto parts_of = [&](int i) { return p.item_parts[row * p.head_chunks + i / 16]; };
   auto part_at = [&](const int2& q, int i, int j) {
@@ -740,7 +771,7 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
     const int2 q = parts_of(i);
     float l2 = INFINITY;
     if (q.y == 1) {
-      if (p.scores != nullptr) l2 = p.row_lse2[bg0 + i];
+      if (p.scores != nullptr) l2 = p.row_lse2[bg0 + i];   // several items: the weights are still to do
     } else {
       float top = -INFINITY, sum = 0.f;
       for (int j = lane; j < q.y; j += 32) {
@@ -793,7 +824,7 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
     }
     __syncthreads();
   }
-  if (p.scores == nullptr) return;
+  if (done) return;
 
   // weights: four slots (of one page) per thread and step.
   const int page_mask = (1 << p.c.page_shift) - 1;
@@ -832,11 +863,15 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
   }
 }
 
-// Whole items, one CTA each and no second kernel, where rows are short
-// (WHOLE_MEASURED); else as many shares as CTAs fit on 148 SMs; 0 CTAs: too
-// many.
+// Whole items, one CTA each and no second kernel, where rows are short: up to
+// 512 slots (1 x 8 rows of 512: 9.2 us against 10.8 in shares; 64 x 8: 29 and
+// 33), up to 1,024 if there are many (16 x 8 rows of 1,000: 16.4 and 22.8, but
+// 1 x 8: 14.9 and 11.4).  Longer rows of different lengths would leave the SMs
+// to the longest one.  Else as many shares as CTAs fit on 148 SMs (with two
+// to four times as many: bf16 1 to 2% faster at 64 x 8 rows of 4,032 slots, 8
+// x 8 rows 10 to 30% slower); 0 CTAs: too many.
 DecodeSplit paged_split(int64_t items, int capacity, int head_dim, bool f8, bool wide, bool may_be_whole) {
-  if (may_be_whole && capacity <= 512) return {static_cast<int>(items), true};
+  if (may_be_whole && (capacity <= 512 || (capacity <= 1024 && items >= 64))) return {static_cast<int>(items), true};
   const int per_sm = head_dim == 128 ? (f8 ? Tile<128, true>::ctas(wide) : Tile<128, false>::ctas(wide))
                                      : (f8 ? Tile<64, true>::ctas(wide) : Tile<64, false>::ctas(wide));
   const int64_t sizes = items * ((capacity + kPdBlock - 1) / kPdBlock + kPdItem);
@@ -859,7 +894,7 @@ static cudaError_t launch_decode_of(const PagedDecodeParams& p, cudaStream_t str
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const int most = p.scores != nullptr ? (p.c.capacity + kPjSlots - 1) / kPjSlots : std::min(p.group, 16);
   const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (148 * 6 + rows - 1) / rows)));
-  return launch_paged(paged_join_kernel<D>, dim3(static_cast<unsigned>(rows), parts), dim3(kPjThreads), 0, 1, stream, p);
+  return launch_paged(paged_join_kernel<D, Tile<D, kF8>::kSums>, dim3(static_cast<unsigned>(rows), parts), dim3(kPjThreads), 0, 1, stream, p);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int head_dim, bool f8, cudaStream_t stream) {
