@@ -2,17 +2,17 @@
 // accumulated attention weight, sm_100a.
 //
 // A row (sequence, KV head) is handled by a cluster of 1 to 8 CTAs, each of
-// which looks at a slice of the row's slots.  What a slot is worth is one
-// 64-bit key, smaller = evicted earlier: the order-preserving bits of the
-// weight (NaN lowest), then 2^31 - 1 - position; slots that may not go (sinks,
-// recent tokens) have the key 2^64 - 1.  One token in, one out (the steady
-// state of decoding) is an argmin over the keys, bound by the bytes of weights
-// and positions.  Several out is an exact radix select of the e-th smallest
-// key over keys in shared memory, in digits of 11 bits (a weight's first
-// digit is its exponent and two bits more, which spreads real weights over
-// many counters): the cluster adds its histograms through distributed shared
-// memory, and stops as soon as a digit's bucket is taken whole, mostly after
-// two.  Everything is integer, so the result is exact and depends on no order.
+// which looks at a slice of the row's slots.  Slots go in the order of their
+// key, smaller = earlier: the order-preserving bits of the weight (NaN lowest),
+// then, among equal weights, 2^31 - 1 - position; slots that may not go (sinks,
+// recent tokens) have a key that no weight has.  One token in, one out (the
+// steady state of decoding) is an argmin, bound by the bytes of weights and
+// positions.  Several out is an exact radix select of the e-th smallest key
+// over keys in shared memory, in digits of 11 bits (a weight's first digit is
+// its exponent and two bits more, which spreads real weights over many
+// counters): the cluster adds its histograms through distributed shared memory,
+// and stops as soon as a digit's bucket is taken whole, mostly after two.
+// Everything is integer, so the result is exact and depends on no order.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -25,13 +25,13 @@ namespace kvpop {
 namespace cg = cooperative_groups;
 
 constexpr int kPaMaxSlice = 16384;     // keys one CTA holds at most (128 KiB); 8 x 16384 = the largest capacity
-// Place of key i: the 16 of a 128-byte line permuted by the line's number, so that threads that each read
-// consecutive keys meet different banks.
-__device__ __forceinline__ int placed(int i) { return i ^ ((i >> 4) & 15); }
+// Place of key i: the 8 words of 4 in a 128-byte line are permuted by the line's number, so that threads that each
+// read consecutive keys meet different banks, and 4 keys stay together.
+__device__ __forceinline__ int placed(int i) { return i ^ ((i >> 3) & 28); }
 constexpr int kPaBits = 11;           // of a digit
 constexpr int kPaBins = 1 << kPaBits;
 constexpr int kPaList = kPaBins * 4 / static_cast<int>(sizeof(RowEntry));   // as the histogram
-constexpr uint64_t kStays = ~0ull;
+constexpr uint32_t kStays = ~0u;       // key of a slot that may not go; no weight has it
 
 // Larger float -> larger key, never 2^32 - 1; -0 equals +0 (the addition makes it +0); NaN -> 0, below every number
 // (the addition's NaN is the canonical 0x7fffffff, whose key 2^32 - 1 wraps to 0 with the one added to all).
@@ -91,11 +91,11 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
   constexpr int kPaWarps = kPaThreads / 32;
   cg::cluster_group cluster = cg::this_cluster();
   const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  extern __shared__ __align__(16) uint64_t keys[];       // kChunk: this CTA's slice; then the rows to write
+  extern __shared__ __align__(16) uint32_t keys[];       // kChunk: weights' keys of this CTA's slice, then its positions
   __shared__ Candidate best[kPaWarps + 1];               // one out: of each warp; [kPaWarps] = of the CTA
   __shared__ __align__(16) uint32_t hist[kChunk ? kPaBins : 4];   // a pass's histogram, read by the cluster
-  __shared__ __align__(16) uint32_t vary[4];             // AND and OR of a pass's keys, high and low halves
-  __shared__ uint64_t every_any[2];                      // the same of the whole cluster
+  __shared__ uint32_t vary[2];                           // AND and OR of a pass's keys, read by the cluster
+  __shared__ uint32_t every_any[2];                      // the same of the whole cluster
   __shared__ uint32_t sel[3];
   __shared__ uint32_t ranks[3];                          // victims before this slice, victims in all, undecided before it
   __shared__ uint32_t taken_here[2];                     // kChunk: victims and undecided in this slice, read by the cluster
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
     return;
   }
   const int cap = p.c.capacity, n = min(count, cap), f = min(m, cap - n), e = m - f;
-  // Tokens at positions sinks .. recent - 1 may go: recent is where the window begins once the new ones are in.
+  // Tokens at positions sinks .. recent - 1 may go: recent is where the window begins once the new ones are in.  Smaller
+  // positions less sinks wrap to numbers from 2^31 - sinks up, which no span exceeds.
   const int64_t recent = static_cast<int64_t>(seen) + m - p.window;
   const uint32_t span = static_cast<uint32_t>(max(int64_t(0), min(recent, int64_t(1) << 31) - p.sinks));
   const int s0 = min(n, cta * p.slice), s1 = min(n, s0 + p.slice);
@@ -147,11 +148,6 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
 
   auto meta_at = [&](int page, int off) {
     return ((static_cast<int64_t>(page) * p.c.n_kv_heads + h) << p.c.page_shift) + off;
-  };
-  auto key_of = [&](float w, int pos) {
-    // Positions below sinks wrap to numbers from 2^31 - sinks up, which no span exceeds.
-    const bool goes = static_cast<uint32_t>(pos) - static_cast<uint32_t>(p.sinks) < span;
-    return goes ? (static_cast<uint64_t>(weight_key(w)) << 32) | static_cast<uint32_t>(0x7fffffff - pos) : kStays;
   };
   // Token i of the sequence into `slot` (< 0: none for it), where position `old` goes (-1: nothing does).
   auto place = [&](int i, int slot, int old) {
@@ -250,6 +246,7 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
   } else {
     // Rows to write, up to kPaList at a time, where the histogram is at other times.
     RowEntry* list = reinterpret_cast<RowEntry*>(hist);
+    int32_t* spots = reinterpret_cast<int32_t*>(keys) + (p.slice + 31) / 32 * 32;
     // Tokens for free slots: an even share for each CTA of the cluster.
     if (f > 0) {
       const int share = (f + ctas - 1) / ctas, f0 = min(f, cta * share), f1 = min(f, f0 + share);
@@ -262,28 +259,26 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
       }
     }
     if (e > 0) {
-      // Radix select, smallest first.  A key with (key & mask) < prefix is taken, one with == prefix is undecided.
-      // Each pass counts a digit and also finds which bits vary among the undecided keys, so that the next digit
-      // starts at the first one that does: weights that are all equal cost one pass, not three, before positions
-      // decide.  The first pass counts while the keys arrive.
-      uint64_t prefix = 0, mask = 0;
+      // Radix select, smallest first, over the weights' keys and, where equal weights leave a choice, over the
+      // positions' among those.  A key with (key & mask) < prefix is taken, one with == prefix is undecided.  Each
+      // pass counts a digit and also finds which bits vary among the undecided keys, so that the next digit starts at
+      // the first one that does: keys that are all equal cost one pass, not three.  The first pass counts while the
+      // keys arrive.
       uint32_t need = static_cast<uint32_t>(e);          // still to take among the undecided
-      bool whole = false;                                // every undecided key is taken
-      int top = 64;                                      // bits top .. 63 are decided
       auto clear = [&] {
         for (int i = tid; i < kPaBins / 4; i += kPaThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-        if (tid == 0) sel[2] = 0;
-        if (tid < 4) vary[tid] = tid < 2 ? ~0u : 0u;
+        if (tid == 0) sel[2] = 0, vary[0] = ~0u, vary[1] = 0u;
         __syncthreads();
       };
       // Counters that many keys share would serialise the lanes: one addition for those that agree with lane 0's key.
       auto count = [&](bool in, uint32_t digit) {
         const uint32_t first = __shfl_sync(0xffffffffu, digit, 0);
-        const uint32_t same = __ballot_sync(0xffffffffu, in && digit == first);
-        if (lane == 0 && same != 0) atomicAdd(&hist[first], static_cast<uint32_t>(__popc(same)));
-        if (in && digit != first) atomicAdd(&hist[digit], 1u);
+        const bool same = in && digit == first;
+        const uint32_t votes = __ballot_sync(0xffffffffu, same);
+        if (lane == 0 && votes != 0) atomicAdd(&hist[first], static_cast<uint32_t>(__popc(votes)));
+        if (in && !same) atomicAdd(&hist[digit], 1u);
       };
-      uint64_t every = ~0ull, any = 0;                   // AND and OR of the undecided keys
+      uint32_t every = ~0u, any = 0;                     // AND and OR of the undecided keys
       clear();
       for (int base = s0; base < s1; base += 4 * kPaThreads * kU) {
         int page[kU];
@@ -296,54 +291,78 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int64_t at = meta_at(max(page[u], 0), (base + 4 * (tid + u * kPaThreads)) & page_mask);
+          const int s = base + 4 * (tid + u * kPaThreads);
+          const int64_t at = meta_at(max(page[u], 0), s & page_mask);
           w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
           x[u] = make_int4(-1, -1, -1, -1);              // a position that never goes
           if (page[u] >= 0) {
             w[u] = *reinterpret_cast<const float4*>(p.c.weight + at);
             x[u] = *reinterpret_cast<const int4*>(p.c.pos + at);
+            if (s + 3 >= s1) {
+              x[u].w = -1;
+              if (s + 2 >= s1) x[u].z = -1;
+              if (s + 1 >= s1) x[u].y = -1;
+            }
           }
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int s = base + 4 * (tid + u * kPaThreads);
+          const int i = base - s0 + 4 * (tid + u * kPaThreads);
           const float wf[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
           const int xi[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          uint32_t k[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint64_t k = s + i < s1 ? key_of(wf[i], xi[i]) : kStays;
-            const bool in = k != kStays;
-            if (s + i < s1 && KVPOP_IN(s + i - s0 < p.slice, p.dbg, DBG_PAGED_APPEND, 4)) keys[placed(s + i - s0)] = k;
-            if (in) every &= k, any |= k;
-            count(in, static_cast<uint32_t>(k >> (64 - kPaBits)));
+          for (int j = 0; j < 4; ++j) {
+            const bool in = static_cast<uint32_t>(xi[j]) - static_cast<uint32_t>(p.sinks) < span;
+            k[j] = in ? weight_key(wf[j]) : kStays;
+            if (in) every &= k[j], any |= k[j];
+            count(in, k[j] >> (32 - kPaBits));
+          }
+          // Slices end at multiples of 8, rows need not: the words past s1 hold keys that stay.
+          if (i < p.slice && KVPOP_IN(i + 4 <= p.slice, p.dbg, DBG_PAGED_APPEND, 4)) {
+            *reinterpret_cast<uint4*>(&keys[placed(i)]) = make_uint4(k[0], k[1], k[2], k[3]);
+            *reinterpret_cast<int4*>(&spots[placed(i)]) = x[u];
           }
         }
       }
-      for (int pass = 0; top > 0; ++pass) {
+      const int here_n = s1 - s0;
+      uint32_t prefix = 0, mask = 0, tied = 0;           // tied: the weights' key whose positions decide
+      bool whole = false, ties = false;                  // every undecided key is taken; positions decide
+      for (int pass = 0, top = 32;; ++pass) {            // bits top .. 31 are decided
+        if (top == 0) {
+          if (ties) break;                               // equal weights and positions: the first `need` in slot order
+          ties = true;
+          tied = prefix;
+          // Positions that may go are below `recent`: 2^31 - 1 less one of them has ones from their bits up to bit 30.
+          top = 32 - __clz(static_cast<int>(static_cast<uint32_t>(min(recent, int64_t(1) << 31) - 1) & 0x7fffffffu));
+          mask = ~((1u << top) - 1u);
+          prefix = 0x7fffffffu & mask;
+          if (top == 0) break;                           // only position 0 may go
+        }
         const int bits = min(top, kPaBits), shift = top - bits;
         if (pass > 0) {
-          sync_row();      // every CTA has read this one's counters
+          sync_row();          // every CTA has read this one's counters
           clear();
-          every = ~0ull, any = 0;
-          for (int base = 0; base < s1 - s0; base += kPaThreads) {
+          every = ~0u, any = 0;
+          for (int base = 0; base < here_n; base += kPaThreads) {
             const int i = base + tid;
-            const uint64_t k = i < s1 - s0 ? keys[placed(i)] : kStays;
-            const bool in = k != kStays && (k & mask) == prefix;
+            uint32_t k = i < here_n ? keys[placed(i)] : kStays;
+            bool in = k != kStays;
+            if (ties) {
+              in = k == tied;
+              if (in) k = 0x7fffffffu - static_cast<uint32_t>(spots[placed(i)]);
+            }
+            in = in && (k & mask) == prefix;
             if (__ballot_sync(0xffffffffu, in) == 0) continue;
             if (in) every &= k, any |= k;
-            count(in, static_cast<uint32_t>(k >> shift) & ((1u << bits) - 1));
+            count(in, (k >> shift) & ((1u << bits) - 1));
           }
         }
         {
-          const uint32_t a1 = __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(every >> 32));
-          const uint32_t a0 = __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(every));
-          const uint32_t o1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32));
-          const uint32_t o0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+          const uint32_t a1 = __reduce_and_sync(0xffffffffu, every), o1 = __reduce_or_sync(0xffffffffu, any);
           if (lane == 0) {
             atomicAnd(&vary[0], a1);
-            atomicAnd(&vary[1], a0);
-            atomicOr(&vary[2], o1);
-            atomicOr(&vary[3], o0);
+            atomicOr(&vary[1], o1);
           }
         }
         sync_row();
@@ -370,11 +389,14 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
           }
         }
         if (warp == 0) {
-          uint4 v = make_uint4(~0u, ~0u, 0u, 0u);
-          if (lane < ctas) v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(vary, lane));
-          v.x = __reduce_and_sync(0xffffffffu, v.x), v.y = __reduce_and_sync(0xffffffffu, v.y);
-          v.z = __reduce_or_sync(0xffffffffu, v.z), v.w = __reduce_or_sync(0xffffffffu, v.w);
-          if (lane == 0) every_any[0] = (static_cast<uint64_t>(v.x) << 32) | v.y, every_any[1] = (static_cast<uint64_t>(v.z) << 32) | v.w;
+          uint32_t v0 = ~0u, v1 = 0u;
+          if (lane < ctas) {
+            const uint32_t* v = cluster.map_shared_rank(vary, lane);
+            v0 = v[0], v1 = v[1];
+          }
+          v0 = __reduce_and_sync(0xffffffffu, v0);
+          v1 = __reduce_or_sync(0xffffffffu, v1);
+          if (lane == 0) every_any[0] = v0, every_any[1] = v1;
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) all += c[i];
@@ -405,8 +427,8 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
           whole = true;
           break;
         }
-        prefix |= static_cast<uint64_t>(sel[0]) << shift;
-        mask |= ((uint64_t(1) << bits) - 1) << shift;
+        prefix |= sel[0] << shift;
+        mask |= ((1u << bits) - 1) << shift;
         need = sel[1];
         if (state == 2) {
           whole = true;
@@ -414,26 +436,30 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
         }
         // The undecided keys agree in every bit from `shift` up now; of those below, skip the ones in which not even
         // this pass's keys differed.
-        every = every_any[0];
-        const uint64_t below = shift == 0 ? 0 : (every ^ every_any[1]) & ((uint64_t(1) << shift) - 1);
-        const int next = below == 0 ? 0 : 64 - __clzll(static_cast<long long>(below));
-        const uint64_t agreed = shift == 0 ? 0 : ((uint64_t(1) << shift) - 1) & ~((uint64_t(1) << next) - 1);
-        prefix |= every & agreed;
+        const uint32_t low = (1u << shift) - 1u, differ = (every_any[0] ^ every_any[1]) & low;
+        top = 32 - __clz(static_cast<int>(differ));
+        const uint32_t agreed = low & ~(top == 32 ? ~0u : (1u << top) - 1u);
+        prefix |= every_any[0] & agreed;
         mask |= agreed;
-        top = next;
         __syncthreads();                                 // the shared words of this pass are read
       }
-      // Victims of this slice: those below the prefix, and of the undecided all or (equal keys, which need equal
-      // positions) the first `need` in slot order.  A thread looks at `per` consecutive slots and remembers what it
-      // saw in a bit each.
-      const int per = (p.slice + kPaThreads - 1) / kPaThreads;         // <= 32: the host gives long slices 512 threads
-      const int i0 = tid * per;
+      // Victims of this slice: those below the prefix, and of the undecided all or (equal keys and positions) the
+      // first `need` in slot order.  A thread looks at `per` consecutive slots and remembers what it saw in a bit each.
+      const int per = (p.slice + kPaThreads - 1) / kPaThreads;         // <= 32: the host gives long slices more threads
+      const int i0 = tid * per, in_thread = max(0, min(per, here_n - i0));
       uint32_t below_bits = 0, equal_bits = 0;
-      for (int j = 0; j < per && i0 + j < s1 - s0; ++j) {
-        const uint64_t k = keys[placed(i0 + j)];
-        const uint64_t head = k & mask;
-        below_bits |= static_cast<uint32_t>(k != kStays && (head < prefix || (whole && head == prefix))) << j;
-        equal_bits |= static_cast<uint32_t>(k != kStays && !whole && head == prefix) << j;
+      if (!ties) {
+        const uint32_t last = min(prefix | ~mask, kStays - 1u);        // the largest key that is taken
+        for (int j = 0; j < in_thread; ++j) below_bits |= static_cast<uint32_t>(keys[placed(i0 + j)] <= last) << j;
+      } else {
+        for (int j = 0; j < in_thread; ++j) {
+          const uint32_t k = keys[placed(i0 + j)];
+          below_bits |= static_cast<uint32_t>(k < tied) << j;
+          if (k != tied) continue;
+          const uint32_t head = (0x7fffffffu - static_cast<uint32_t>(spots[placed(i0 + j)])) & mask;
+          below_bits |= static_cast<uint32_t>(head < prefix || (whole && head == prefix)) << j;
+          equal_bits |= static_cast<uint32_t>(!whole && head == prefix) << j;
+        }
       }
       // Exclusive scans over the block, below and equal in a word (at most 1,024 of each in a warp), and the totals.
       const uint32_t own = __popc(below_bits) | (__popc(equal_bits) << 16);
@@ -494,7 +520,8 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
         uint32_t at = first - static_cast<uint32_t>(done);                  // wraps: outside the list
         for (uint32_t bits = goes; bits != 0; bits &= bits - 1, ++at) {
           const int i = i0 + __ffs(bits) - 1;
-          if (at < kPaList && KVPOP_IN(s0 + i < n, p.dbg, DBG_PAGED_APPEND, 5)) list[at] = {s0 + i, 0x7fffffffu - static_cast<uint32_t>(keys[placed(i)])};
+          if (at < kPaList && KVPOP_IN(s0 + i < n, p.dbg, DBG_PAGED_APPEND, 5))
+            list[at] = {s0 + i, static_cast<uint32_t>(spots[placed(i)])};
         }
         __syncthreads();
         const int entries = min(here - done, kPaList);
@@ -696,7 +723,7 @@ constexpr int kPsRows = 3 * 148;     // more rows than this are streamed
 // SMs would have no CTA and slices are over 2,048 slots: every pass of the
 // select is a barrier of the cluster, and larger clusters wait for room
 // (24 x 8 rows of 16,000 slots: 47, 41, 56 and 121 us with 1, 2, 4 and 8 CTAs
-// per row; 4 x 8 rows: 35, 23 and 33 us with 1, 4 and 8).
+// per row, since then 38 with 2; 4 x 8 rows: 35, 23 and 33 us with 1, 4 and 8).
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const bool chunk = !p.one_each;
@@ -720,10 +747,10 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
     while (ctas > 1 && (rows * ctas > 2 * 148 || p.c.capacity < 1024 * ctas)) ctas >>= 1;
   }
   p.slice = ((p.c.capacity + ctas - 1) / ctas + 7) / 8 * 8;
-  // Many short slices take 256 threads, so that four CTAs share an SM (200 x 8 rows of 1,000 slots: 70 us, with 512
+  // Many short slices take 256 threads, so that four CTAs share an SM (200 x 8 rows of 1,000 slots: 65 us, with 512
   // threads 87; 8 rows of 16,000 slots: 15 and 13).
-  const bool small = !chunk || (p.slice <= 2048 && rows * ctas > 2 * 148);
-  const size_t smem = chunk ? static_cast<size_t>(p.slice + 15) / 16 * 128 : 0;
+  const bool small = !chunk || (p.slice <= 4096 && rows * ctas > 2 * 148);
+  const size_t smem = chunk ? static_cast<size_t>(p.slice + 31) / 32 * 256 : 0;
   const dim3 grid(static_cast<unsigned>(rows * ctas)), block(small ? 256 : 512);
   static std::atomic<uint64_t> ready[8];
   auto go = [&](auto kern, int which) {
