@@ -244,7 +244,7 @@ def paged_append_kv(k_new, v_new, cache: PagedCache, window: int, sinks: int, cu
     if evicted is not None:
         _check_given(evicted, (T, H), torch.int32, dev, "evicted")
     elif stream is None:
-        evicted = torch.empty((T, H), dtype=torch.int32, device=cache.device)
+        evicted = k_new.new_empty((T, H), dtype=torch.int32)
     else:
         with _on_stream(stream):
             evicted = torch.empty((T, H), dtype=torch.int32, device=cache.device)

@@ -173,6 +173,77 @@ def test_two_threads_on_two_streams():
         ref.assert_same_state(pairs[i][0], {n: alone[i][1][n].cpu() for n in ("k_pages", "v_pages", "pos", "weight", "count", "seen")})
 
 
+def test_eight_bits_without_scales():
+    """No scales are scales of 1, each on its own."""
+    for drop in (("k_scale", "v_scale"), ("k_scale",), ("v_scale",)):
+        a = ref.make_cache(2, 2, 64, 16, 600, "e4m3", seed=3)
+        for name in drop:
+            a[name] = None
+        T = 700
+        k, v = (torch.randn(T, 2, 64, generator=gen(s)).to(torch.bfloat16) for s in (1, 2))
+        want = ref.compact(a, k, v, None, [0, 500, T], None)
+        kv.paged_compact_kv(k.cuda(), v.cuda(), None, [0, 500, T], kv.PagedCache(**a))
+        ref.assert_same_state(a, want)
+        base.check_append(a, None, 16, 4, seed=1)
+        base.check_append(a, [0, 3, 9], 16, 4, seed=2)
+        q = torch.randn(2, 6, 64, generator=gen(5)).to(torch.bfloat16).cuda()
+        base.check_decode(a, q, 0.3, True)
+
+
+def test_binding_refuses():
+    """Wrong types, shapes, layouts and sizes raise before anything is enqueued, and change nothing."""
+    a = ref.make_cache(2, 2, 64, 16, 100, seed=1)
+    base.fill_random(a, [[100, 20], [0, 5]], seed=1)
+    before = {n: ref.as_bytes(a[n]).copy() for n in ("k_pages", "v_pages", "pos", "weight", "count", "seen")}
+    cache = kv.PagedCache(**a)
+    dev = "cuda"
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=dev)
+    kn = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=dev)
+    T = 30
+    k = torch.zeros(T, 2, 64, dtype=torch.bfloat16, device=dev)
+    keep, score = torch.ones(2, T, dtype=torch.uint8, device=dev), torch.zeros(2, T, device=dev)
+    wide = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device=dev)
+    bad_caches = [
+        dict(k_pages=a["k_pages"].float()), dict(v_pages=a["v_pages"][:-1]), dict(k_pages=a["k_pages"][..., ::2]),
+        dict(k_pages=a["k_pages"][:1].expand(a["k_pages"].shape)), dict(page_table=a["page_table"].long()),
+        dict(page_table=a["page_table"][:, ::2]), dict(count=a["count"][:1]), dict(count=a["count"].float()),
+        dict(seen=a["seen"].cpu()), dict(pos=a["pos"].long()), dict(weight=a["weight"].double()), dict(capacity=0),
+        dict(capacity=10 ** 6), dict(k_scale=torch.ones(2, device=dev)),
+    ]
+    for kw in bad_caches:
+        with pytest.raises((TypeError, ValueError)):
+            kv.PagedCache(**{**a, **kw})
+    decode, append, compact = kv.paged_decode_attention, kv.paged_append_kv, kv.paged_compact_kv
+    no_weight = kv.PagedCache(**{**a, "weight": None})
+    small = torch.empty(16, dtype=torch.uint8, device=dev)
+    bad_calls = [
+        lambda: decode(q.float(), cache), lambda: decode(q[:1], cache), lambda: decode(q[:, :3], cache),
+        lambda: decode(q.cpu(), cache), lambda: decode(wide[..., ::2], cache), lambda: decode(q[:, :, :32], cache),
+        lambda: decode(q, cache, out=q.float()), lambda: decode(q, cache, lse=torch.empty(2, 3, device=dev)),
+        lambda: decode(q, cache, accumulate=True, workspace=small), lambda: decode(q, cache, scale=0.0),
+        lambda: decode(q, cache, scale=float("inf")), lambda: decode(q, no_weight, accumulate=True),
+        lambda: decode(q, cache, status=torch.zeros(1, device=dev)),
+        lambda: append(kn[:1], kn, cache, 4, 2), lambda: append(kn, kn.float(), cache, 4, 2),
+        lambda: append(kn, wide[:, :2, :64], cache, 4, 2), lambda: append(kn, kn, cache, -1, 2),
+        lambda: append(kn, kn, cache, 100, 2), lambda: append(kn, kn, cache, 4, 2, cu_new=[0, 1]),
+        lambda: append(kn, kn, cache, 4, 2, cu_new=[0, 2, 1]), lambda: append(kn, kn, cache, 1, 2, cu_new=[0, 0, 2]),
+        lambda: append(kn, kn, cache, 4, 2, cu_new=[0, 2 ** 40, 2]), lambda: append(kn, kn, no_weight, 4, 2),
+        lambda: append(kn, kn, cache, 4, 2, evicted=torch.empty(2, 3, dtype=torch.int32, device=dev)),
+        lambda: compact(k, k[:-1], keep, [0, 10, T], cache), lambda: compact(k, k, keep[:1], [0, 10, T], cache),
+        lambda: compact(k, k, keep, [0, T], cache), lambda: compact(k, k, keep, [0, 10, T - 1], cache),
+        lambda: compact(k, k, keep, [0, 20, 10], cache), lambda: compact(k, k, keep.float(), [0, 10, T], cache),
+        lambda: compact(k, k, keep, [0, 10, T], cache, score=score.double()),
+        lambda: compact(k, k, keep, [0, 10, T], no_weight, score=score),
+    ]
+    for i, call in enumerate(bad_calls):
+        with pytest.raises((TypeError, ValueError, kv.KvpopError)):
+            call()
+            pytest.fail(f"call {i} was taken")
+    torch.cuda.synchronize()
+    for n, x in before.items():
+        assert np.array_equal(ref.as_bytes(a[n]), x)
+
+
 FIRST_CALL = """
 import sys
 sys.path[:0] = [{root!r}, {tests!r}]
