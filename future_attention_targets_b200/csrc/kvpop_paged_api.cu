@@ -7,8 +7,6 @@
 #include <stdio.h>
 
 #include <algorithm>
-#include <memory>
-#include <new>
 
 #include "kvpop_host.h"
 #include "kvpop_paged.cuh"

@@ -46,6 +46,28 @@ struct Candidate {
   uint32_t key;
   int pos, at;
 };
+// Looks at four slots from s on, weights' bits w and positions x.  From +0 to +inf a weight's key is its bits plus
+// 2^31 + 1; others take the long way.
+__device__ __forceinline__ void consider(Candidate& c, const uint4& w, const int4& x, int s, uint32_t sinks, uint32_t span) {
+  const uint32_t wu[4] = {w.x, w.y, w.z, w.w};
+  const int xi[4] = {x.x, x.y, x.z, x.w};
+  uint32_t k[4];
+  if (max(max(w.x, w.y), max(w.z, w.w)) <= 0x7f800000u) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = wu[e] + 0x80000001u;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = weight_key(__uint_as_float(wu[e]));
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (static_cast<uint32_t>(xi[e]) - sinks >= span) k[e] = ~0u;       // with this key a candidate is none
+    const bool better = (k[e] < c.key) | ((k[e] == c.key) & (xi[e] > c.pos));
+    c.key = better ? k[e] : c.key;
+    c.pos = better ? xi[e] : c.pos;
+    c.at = better ? s + e : c.at;
+  }
+}
 __device__ __forceinline__ Candidate first_to_go(const Candidate& c) {
   Candidate r;
   r.key = __reduce_min_sync(0xffffffffu, c.key);
@@ -173,7 +195,7 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
     if (e > 0) {
       Candidate c = {~0u, -1, -1};
       for (int base = s_lo + 4 * tid; base < s1; base += 4 * kPaThreads * kU) {
-        float4 w[kU];
+        uint4 w[kU];
         int4 x[kU];
         if (base != s_lo + 4 * tid)
 #pragma unroll
@@ -185,11 +207,11 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
         for (int u = 0; u < kU; ++u) {
           const int s = base + u * 4 * kPaThreads;
           x[u] = make_int4(-1, -1, -1, -1);              // a position that never goes
-          w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          w[u] = make_uint4(0, 0, 0, 0);
           if (s < s1) {
             if (static_cast<uint32_t>(raw[u]) < static_cast<uint32_t>(p.c.n_pages)) {
               const int64_t from = meta_at(raw[u], s & page_mask);
-              w[u] = *reinterpret_cast<const float4*>(p.c.weight + from);
+              w[u] = *reinterpret_cast<const uint4*>(p.c.weight + from);
               x[u] = *reinterpret_cast<const int4*>(p.c.pos + from);
               if (s + 3 >= s1) {
                 x[u].w = -1;
@@ -202,19 +224,7 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
           }
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const float wf[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-          const int xi[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool goes = static_cast<uint32_t>(xi[i]) - static_cast<uint32_t>(p.sinks) < span;
-            const uint32_t k = goes ? weight_key(wf[i]) : ~0u;
-            const bool better = (k < c.key) | ((k == c.key) & (xi[i] > c.pos) & goes);
-            c.key = better ? k : c.key;
-            c.pos = better ? xi[i] : c.pos;
-            c.at = better ? base + u * 4 * kPaThreads + i : c.at;
-          }
-        }
+        for (int u = 0; u < kU; ++u) consider(c, w[u], x[u], base + u * 4 * kPaThreads, static_cast<uint32_t>(p.sinks), span);
       }
       c = first_to_go(c);
       if (lane == 0) best[warp] = c;
@@ -666,23 +676,14 @@ __global__ void __launch_bounds__(kPsThreads, 3) paged_append_stream_kernel(cons
       for (int i = 0; i < kPsU; ++i) {
         if (((here >> i) & 1) == 0) continue;
         const int s = now.part * kPsSlots + 4 * (tid + i * kPsThreads);
-        const uint4 w = sm.words[parity][0][i][tid], x = sm.words[parity][1][i][tid];
-        const uint32_t wu[4] = {w.x, w.y, w.z, w.w};
-        int xi[4] = {static_cast<int>(x.x), static_cast<int>(x.y), static_cast<int>(x.z), static_cast<int>(x.w)};
+        const uint4 w = sm.words[parity][0][i][tid];
+        int4 x = *reinterpret_cast<const int4*>(&sm.words[parity][1][i][tid]);
         if (s + 3 >= cap) {
-          xi[3] = -1;
-          if (s + 2 >= cap) xi[2] = -1;
-          if (s + 1 >= cap) xi[1] = -1;
+          x.w = -1;
+          if (s + 2 >= cap) x.z = -1;
+          if (s + 1 >= cap) x.y = -1;
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool goes = static_cast<uint32_t>(xi[e]) - static_cast<uint32_t>(p.sinks) < span;
-          const uint32_t k = goes ? weight_key(__uint_as_float(wu[e])) : ~0u;
-          const bool better = (k < c.key) | ((k == c.key) & (xi[e] > c.pos) & goes);
-          c.key = better ? k : c.key;
-          c.pos = better ? xi[e] : c.pos;
-          c.at = better ? s + e : c.at;
-        }
+        consider(c, w, x, s, static_cast<uint32_t>(p.sinks), span);
       }
     }
     if (now.part == steps - 1) {                          // the row's last step
