@@ -718,13 +718,16 @@ __global__ void __launch_bounds__(kPsThreads, 3) paged_append_stream_kernel(cons
 
 constexpr int kPsRows = 3 * 148;     // more rows than this are streamed
 
-// CTAs per row.  One out: the largest of 8, 4, 2, 1 whose clusters leave two
-// CTAs per SM at most and 1,024 slots per CTA at least.  Several out: the
-// fewest that leave slices of 8,192 slots at most, and more while half the
-// SMs would have no CTA and slices are over 2,048 slots: every pass of the
-// select is a barrier of the cluster, and larger clusters wait for room
-// (24 x 8 rows of 16,000 slots: 47, 41, 56 and 121 us with 1, 2, 4 and 8 CTAs
-// per row, since then 38 with 2; 4 x 8 rows: 35, 23 and 33 us with 1, 4 and 8).
+// CTAs per row.  One out: the largest of 8, 4, 2, 1 that leaves 1,024 slots per
+// CTA at least, and two CTAs per SM at most or 8,192 slots per CTA (16 x 5
+// rows of 96,250 slots: 26 us with 8 CTAs per row, 39 with 2).  Several out:
+// the fewest that leave slices of 8,192 slots at most (12,800 for many rows,
+// rather than 4 CTAs per row: 86 x 4 rows of 23,581 slots 85 and 109 us), and
+// more while half the SMs would have no CTA and slices are over 2,048 slots:
+// every pass of the select is a barrier of the cluster, and larger clusters
+// wait for room (24 x 8 rows of 16,000 slots: 47, 41, 56 and 121 us with 1, 2,
+// 4 and 8 CTAs per row, since then 38 with 2; 4 x 8 rows: 35, 23 and 33 us with
+// 1, 4 and 8).
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const bool chunk = !p.one_each;
@@ -742,10 +745,11 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
   }
   int ctas = 1;
   if (chunk) {
-    while (ctas < 8 && (p.c.capacity > 8192 * ctas || (rows * ctas <= 74 && p.c.capacity > 2048 * ctas))) ctas <<= 1;
+    const int most = p.c.capacity > 2 * 8192 && rows * 4 > 2 * 148 ? 12800 : 8192;      // at 12,800 two still share an SM
+    while (ctas < 8 && (p.c.capacity > most * ctas || (rows * ctas <= 74 && p.c.capacity > 2048 * ctas))) ctas <<= 1;
   } else {
     ctas = 8;
-    while (ctas > 1 && (rows * ctas > 2 * 148 || p.c.capacity < 1024 * ctas)) ctas >>= 1;
+    while (ctas > 1 && (p.c.capacity < 1024 * ctas || (rows * ctas > 2 * 148 && p.c.capacity < 8192 * ctas))) ctas >>= 1;
   }
   p.slice = ((p.c.capacity + ctas - 1) / ctas + 7) / 8 * 8;
   // Many short slices take 256 threads, so that four CTAs share an SM (200 x 8 rows of 1,000 slots: 65 us, with 512
