@@ -82,6 +82,8 @@ struct PagedCompactParams {
   int32_t start[kMaxSeqs + 1];
 };
 
+// The kernels are programmatic dependents: they may be resident while the one before still writes what they read.  The
+// wait orders ordinary loads behind those writes, not non-coherent ones (__ldg), so there are none of those.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kPaThreads, 1024 / kPaThreads) paged_append_ke
     }
     if (cta == 0 && tid < D / 4) {
       const uint16_t* from = (tid < D / 8 ? p.k_new : p.v_new) + tok0 * p.token_stride + static_cast<int64_t>(h) * D + 8 * (tid % (D / 8));
-      fresh = __ldg(reinterpret_cast<const uint4*>(from));
+      fresh = *reinterpret_cast<const uint4*>(from);
     }
   }
   const int count = p.c.count[row], seen = p.c.seen[row];

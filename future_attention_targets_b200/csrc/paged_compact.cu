@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kPcThreads, kF8 ? 5 : 4) paged_compact_kernel(
     auto bits = [](uint32_t x) { return __popc((((x & 0x7f7f7f7fu) + 0x7f7f7f7fu) | x) & 0x80808080u); };
 #pragma unroll 8
     for (int i = tid; i < words; i += kPcThreads) {
-      const uint4 x = __ldg(v + i);
+      const uint4 x = v[i];
       c += bits(x.x) + bits(x.y) + bits(x.z) + bits(x.w);
     }
     for (int i = tid; i < head; i += kPcThreads) c += mask[i] != 0;

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
       const int d0 = kF8 ? 64 * (j / 2) + 16 * t + 8 * (j & 1) : 32 * j + 8 * t, head = g + 8 * r;
       qw[r][j] = make_uint4(0, 0, 0, 0);
       if (head < G)
-        qw[r][j] = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_stride + static_cast<int64_t>(h * p.group + hc * 16 + head) * D + d0));
+        qw[r][j] = *reinterpret_cast<const uint4*>(p.q + b * p.q_stride + static_cast<int64_t>(h * p.group + hc * 16 + head) * D + d0);
     }
   stage_pages(0);
 #pragma unroll
