@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kPsThreads, 3) paged_append_stream_kernel(cons
           const int slot = count < cap ? count : c.key == ~0u ? -1 : c.at;
           write_one<D, kF8>(p, now.b, now.h, now.b, slot, count < cap ? -1 : c.pos, seen, sm.fresh[at][lane]);
           if (lane == 0) {
-            p.c.count[now.row] = min(count + 1, cap);
+            p.c.count[now.row] = min(count, cap - 1) + 1;        // count may be any int32
             p.c.seen[now.row] = seen + 1;
           }
         }
