@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "kvpop_debug.cuh"
+#include "kvpop_host.h"
 #include "kvpop_sched.h"
 
 namespace kvpop {
@@ -220,17 +221,19 @@ __device__ __forceinline__ void copy_rows(const PagedView& c, const uint16_t* k,
   }
 }
 
-// Raises a kernel's dynamic shared memory limit on the current device, once per device (`done`: one bit each).
-// Another thread may do it again at the same time: that changes nothing.
+// The contexts in which a kernel's limit of dynamic shared memory has been raised, by id: a context loads the kernel
+// anew, without the limit.  Ids that share a place raise it again each time they take turns.
+struct SmemReady {
+  std::atomic<unsigned long long> context[16];
+};
+
+// Raises the limit in the current context, once.  Another thread may do it again at the same time: that changes nothing.
 template <class Kern>
-static cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+static cudaError_t allow_smem(Kern kern, size_t bytes, SmemReady& ready) {
+  const unsigned long long id = current_context_id();
+  if (id != 0 && ready.context[id % 16].load(std::memory_order_relaxed) == id) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && id != 0) ready.context[id % 16].store(id, std::memory_order_relaxed);
   return e;
 }
 

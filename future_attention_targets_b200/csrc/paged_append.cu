@@ -734,7 +734,7 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
   if (!chunk && rows > kPsRows) {
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows, 3 * 148))), block(kPsThreads);
     constexpr size_t kPsSmem = sizeof(StreamSmem);
-    static std::atomic<uint64_t> ready[4];
+    static SmemReady ready[4];
     auto go = [&](auto kern, int which) {
       const cudaError_t e = allow_smem(kern, kPsSmem, ready[which]);
       return e != cudaSuccess ? e : launch_paged(kern, grid, block, kPsSmem, 1, stream, p);
@@ -757,7 +757,7 @@ cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cud
   const bool small = !chunk || (p.slice <= 4096 && rows * ctas > 2 * 148);
   const size_t smem = chunk ? static_cast<size_t>(p.slice + 31) / 32 * 256 : 0;
   const dim3 grid(static_cast<unsigned>(rows * ctas)), block(small ? 256 : 512);
-  static std::atomic<uint64_t> ready[8];
+  static SmemReady ready[8];
   auto go = [&](auto kern, int which) {
     if (smem > 0) {
       const cudaError_t e = allow_smem(kern, kPaMaxSlice * 8, ready[which]);

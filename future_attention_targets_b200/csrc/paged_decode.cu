@@ -895,7 +895,7 @@ template <int D, bool kF8>
 static cudaError_t launch_decode_of(const PagedDecodeParams& p, cudaStream_t stream) {
   const dim3 grid(p.ctas), block(kPdThreads);
   constexpr size_t smem = kPdWarps * Tile<D, kF8>::kRing;
-  static std::atomic<uint64_t> ready[2];
+  static SmemReady ready[2];
   auto go = [&](auto kern, int wide) {
     const cudaError_t e = allow_smem(kern, smem, ready[wide]);
     return e != cudaSuccess ? e : launch_paged(kern, grid, block, smem, 1, stream, p);

@@ -15,6 +15,7 @@
 
 #include "kvpop_cache.h"
 #include "kvpop_debug.cuh"
+#include "kvpop_host.h"
 
 namespace kvpop {
 
@@ -689,10 +690,9 @@ static __device__ __align__(256) float g_decode_scratch[kDecodeScratchBytes / si
 
 size_t decode_scratch_bytes() { return kDecodeScratchBytes; }
 
-// Unique id of the calling thread's current CUDA context, or 0 when no
-// context is current or the driver cannot say.  Ids are never reused, so a
-// context created after cudaDeviceReset has a new one.
-static unsigned long long current_context_id() {
+// Ids are never reused, so a context created after cudaDeviceReset has a new
+// one.
+unsigned long long current_context_id() {
   using GetCurrent = CUresult (*)(CUcontext*);
   using GetId = CUresult (*)(CUcontext, unsigned long long*);
   static GetCurrent get_current = nullptr;
