@@ -20,6 +20,7 @@ import array
 import contextlib
 import ctypes
 import math
+import operator
 import os
 
 from . import _binding as _b
@@ -80,6 +81,17 @@ def _host_i32(values, name: str) -> array.array:
         return array.array("i", values)
     except OverflowError:
         raise ValueError(f"{name}: value out of int32 range") from None
+
+
+def _i32(value, name: str) -> int:
+    """A whole number within int32: ctypes would take its low 32 bits of any other."""
+    try:
+        value = operator.index(value)
+    except TypeError:
+        raise TypeError(f"{name} must be a whole number, not {value!r}") from None
+    if not -2**31 <= value < 2**31:
+        raise ValueError(f"{name} ({value}) is out of int32 range")
+    return value
 
 
 def _check_given(t, shape, dtype, device: int, name: str):
@@ -229,6 +241,7 @@ def paged_append_kv(k_new, v_new, cache: PagedCache, window: int, sinks: int, cu
     sequence, over the slots of least accumulated weight where a row is full.  Returns evicted [T_new, H_kv] int32:
     the position each token displaced, -1 for a free slot, -2 if it was not stored."""
     import torch
+    window, sinks = _i32(window, "window"), _i32(sinks, "sinks")
     dev = _check_cache(cache)
     B, H, d = cache.batch, cache.n_kv_heads, cache.head_dim
     if cu_new is None:
@@ -259,8 +272,9 @@ def paged_append_kv(k_new, v_new, cache: PagedCache, window: int, sinks: int, cu
 
 def paged_decode_workspace_bytes(cache: PagedCache, n_q_heads: int, accumulate: bool | None = None) -> int:
     """Device workspace of paged_decode_attention (accumulate: whether weights are, by default if the cache has any)."""
+    n_q_heads = _i32(int(n_q_heads), "n_q_heads")
     accumulate = cache.weight is not None if accumulate is None else accumulate
-    return int(paged_lib().kvpop_paged_decode_workspace_bytes(cache.struct, int(n_q_heads), int(accumulate)))
+    return int(paged_lib().kvpop_paged_decode_workspace_bytes(cache.struct, n_q_heads, 1 if accumulate else 0))
 
 
 def paged_decode_attention(q, cache: PagedCache, scale: float | None = None, accumulate: bool = False, out=None,

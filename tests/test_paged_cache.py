@@ -160,3 +160,19 @@ def test_python_refuses_what_is_no_cache():
                  lambda: kv.paged_compact_kv(cpu, cpu, None, [0, 1], 3)):
         with pytest.raises(TypeError, match="PagedCache"):
             call()
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 4, -2 ** 31 - 1, 4.0, "4", None])
+def test_python_refuses_numbers_that_are_no_int32(value):
+    """A number that does not fit is refused, not cut to its low 32 bits."""
+    calls = [lambda: kv.paged_append_kv(None, None, None, value, 2), lambda: kv.paged_append_kv(None, None, None, 4, value)]
+    if isinstance(value, int):
+        calls.append(lambda: kv.paged_decode_workspace_bytes(None, value))
+    for call in calls:
+        with pytest.raises((TypeError, ValueError), match="window|sinks|n_q_heads"):
+            call()
+
+
+def test_python_takes_whole_numbers_of_any_type():
+    np = pytest.importorskip("numpy")
+    assert [P._i32(x, "x") for x in (np.int64(7), np.uint8(7), True, -2 ** 31, 2 ** 31 - 1)] == [7, 7, 1, -2 ** 31, 2 ** 31 - 1]
