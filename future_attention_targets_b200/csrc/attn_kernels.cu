@@ -812,8 +812,8 @@ __device__ __forceinline__ float dot_bf16_row(const uint16_t* a, const uint16_t*
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
   for (int d = 0; d < HD; d += 8) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a + d));
-    const uint4 y = __ldg(reinterpret_cast<const uint4*>(b + d));
+    const uint4 x = *reinterpret_cast<const uint4*>(a + d);
+    const uint4 y = *reinterpret_cast<const uint4*>(b + d);
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -1475,7 +1475,7 @@ int target_split_groups() { return kColGroups; }
 
 // Normaliser rows [H_q, T] of pass 2 from a given lse [H_q, T] (the
 // standalone pass; the pipelines have pass 1 write them next to lse).
-__global__ void __launch_bounds__(256) norm_rows_kernel(const float* __restrict__ lse, uint4* __restrict__ rows,
+__global__ void __launch_bounds__(256) norm_rows_kernel(const float* lse, uint4* rows,
                                                         int64_t n, float inv_scale, int32_t* dbg) {
 #if KVPOP_PDL_PASSES
   asm volatile("griddepcontrol.wait;" ::: "memory");   // lse comes from the kernel before
@@ -1483,7 +1483,7 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const float* __restrict_
 #endif
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-    if (KVPOP_IN(i >= 0 && i < n, dbg, DBG_NORM_ROWS, 1)) rows[i] = norm_row(__ldg(lse + i), inv_scale);
+    if (KVPOP_IN(i >= 0 && i < n, dbg, DBG_NORM_ROWS, 1)) rows[i] = norm_row(lse[i], inv_scale);
 }
 
 cudaError_t launch_norm_rows(const float* lse, void* rows, int64_t n, float inv_scale, int sm_count, int32_t* dbg,

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) keep_mask_kernel(const __grid
   const int32_t chunk = (hi - lo + kKeepCluster - 1) / kKeepCluster;
   const int32_t s0 = min(hi, lo + r * chunk), s1 = min(hi, s0 + chunk);
   for (int32_t i = s0 + tid; i < s1; i += kKeepThreads)
-    if (in_row(i, 2) && KVPOP_IN(i - s0 < p.key_cap, p.dbg, DBG_KEEP, 3)) keys[i - s0] = order_key(__ldg(score + i));
+    if (in_row(i, 2) && KVPOP_IN(i - s0 < p.key_cap, p.dbg, DBG_KEEP, 3)) keys[i - s0] = order_key(score[i]);
   if (r == 0)
     for (int32_t i = tid; i < S; i += kKeepThreads)
       if (in_row(i, 4)) keep[i] = 1;

@@ -51,7 +51,7 @@ __device__ __forceinline__ int for_each_kept(const uint8_t* mask, int lo, int hi
   const int mid = lo + head, n16 = (hi - mid) >> 4;
   const uint4* v = reinterpret_cast<const uint4*>(mask + mid);
   for (int w = 0; w < n16; ++w) {
-    uint32_t bits = nonzero_mask16(__ldg(v + w));
+    uint32_t bits = nonzero_mask16(v[w]);
     while (bits) {
       const int j = __ffs(bits) - 1;
       bits &= bits - 1;
@@ -72,7 +72,7 @@ __device__ __forceinline__ int count_kept(const uint8_t* mask, int lo, int hi) {
   const int mid = lo + head, n16 = (hi - mid) >> 4;
   const uint4* v = reinterpret_cast<const uint4*>(mask + mid);
   for (int w = 0; w < n16; ++w) {
-    const uint4 x = __ldg(v + w);
+    const uint4 x = v[w];
     n += __popc(nonzero_byte_bits(x.x)) + __popc(nonzero_byte_bits(x.y)) + __popc(nonzero_byte_bits(x.z)) +
          __popc(nonzero_byte_bits(x.w));
   }
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kv_kernel(const __
         const int64_t src = (static_cast<int64_t>(s0 + list_pos[e]) * p.n_kv_heads + h) * d + w * 8;
         buf[u] = KVPOP_IN(list_pos[e] >= 0 && list_pos[e] < L && s0 + list_pos[e] < p.total_tokens, p.dbg,
                           DBG_COMPACT, 3)
-                     ? __ldg(reinterpret_cast<const uint4*>((is_v ? p.v : p.k) + src))
+                     ? __ldcg(reinterpret_cast<const uint4*>((is_v ? p.v : p.k) + src))
                      : make_uint4(0, 0, 0, 0);
       }
     }

@@ -32,3 +32,23 @@ def test_paged_kernels_load_coherently(name):
 def test_every_paged_source_is_looked_at():
     assert sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "paged_*.cu"))) == [
         "paged_append.cu", "paged_compact.cu", "paged_decode.cu"]
+
+
+SOURCES = sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+@pytest.mark.parametrize("name", [n for n in SOURCES if WAITS.search(code_of(n))])
+def test_kernels_that_wait_load_coherently(name):
+    """No source with such a kernel has a non-coherent load; a kernel beside it that is launched without the attribute
+    may say __restrict__."""
+    code = code_of(name)
+    assert not re.search(r"\b__ldg\(|\bld\.global(\.\w+)*\.nc\b", code)
+    for kernel in re.split(r"\b__global__\b", code)[1:]:
+        if WAITS.search(kernel):
+            assert "__restrict__" not in kernel[:kernel.index("{")]
+
+
+def test_launches_with_the_attribute_are_all_looked_at():
+    launching = [n for n in SOURCES if "cudaLaunchAttributeProgrammaticStreamSerialization" in code_of(n)]
+    assert launching == ["attn_kernels.cu", "keep_mask.cu", "kvpop_paged.cuh", "static_cache.cu"]
+    assert all(WAITS.search(code_of(n)) for n in launching)
