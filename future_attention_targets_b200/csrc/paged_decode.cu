@@ -137,6 +137,16 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
   }
 }
 
+// V's scale of head h (1 without one) as a factor from [1, 2) and a power of two, both exact.  The factor goes with the
+// sums, the power with the result: the whole scale over a sum of up to 2^25, or times one, leaves fp32's range long
+// before the result does.  Ordinary scales give the same bits either way.
+__device__ __forceinline__ float2 split_scale(const float* scales, int h) {
+  const float s = scales != nullptr ? scales[h] : 1.f;
+  const float up = s < 0x1p-126f ? 0x1p-64f : 1.f;        // subnormal ones by way of 2^64 times them
+  const uint32_t u = __float_as_uint(s * (1.f / up));
+  return make_float2(__uint_as_float((u & 0x007fffffu) | 0x3f800000u), __uint_as_float(u & 0x7f800000u) * up);
+}
+
 // A tile in shared memory: K rows, then V rows.  Rows of 256 bytes come 16 at a
 // time, shorter ones 32: a step's chain of products, maximum, exponentials and
 // products costs about the same either way, and an e4m3 cache with half the
@@ -620,7 +630,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
       }
     }
   __syncthreads();
-  const float vs = kF8 && p.c.v_scale != nullptr ? p.c.v_scale[h] : 1.f;
+  const float2 vs = kF8 ? split_scale(p.c.v_scale, h) : make_float2(1.f, 1.f);
   const bool all = cnt == n;                              // the whole item: the result; else a part of it
   const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (lo == 0 ? 1 : 0)) * 16;
   KVPOP_CHECK(lo + cnt <= n && n <= p.c.capacity && row < p.c.batch * p.c.n_kv_heads, p.dbg, DBG_PAGED_DECODE, 5);
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
       sm_m[w][i] = f;                                     // the warp's factor
     }
     const float l2 = sum != 0.f ? base - kShift + log2f(sum) : INFINITY;
-    fin[i] = make_float2(all ? (sum != 0.f ? vs / sum : 0.f) : vs, l2);
+    fin[i] = make_float2(all ? (sum != 0.f ? vs.x / sum : 0.f) : vs.x, l2);
     if (all) {
       if (p.lse != nullptr) p.lse[bg0 + i] = sum != 0.f ? l2 * kLn2 : -INFINITY;
       if (!p.whole && p.scores != nullptr) p.row_lse2[bg0 + i] = l2;
@@ -658,8 +668,8 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
     const float f = fin[i].x;
     if (all) {
       const bool some = fin[i].y != INFINITY;
-      const __nv_bfloat162 u = __floats2bfloat162_rn(some ? y.x * f : 0.f, some ? y.y * f : 0.f);
-      const __nv_bfloat162 w = __floats2bfloat162_rn(some ? y.z * f : 0.f, some ? y.w * f : 0.f);
+      const __nv_bfloat162 u = __floats2bfloat162_rn(some ? y.x * f * vs.y : 0.f, some ? y.y * f * vs.y : 0.f);
+      const __nv_bfloat162 w = __floats2bfloat162_rn(some ? y.z * f * vs.y : 0.f, some ? y.w * f * vs.y : 0.f);
       *reinterpret_cast<uint2*>(p.out + (bg0 + i) * D + d) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
     } else {
@@ -740,8 +750,9 @@ constexpr int kPjSlots = 4 * kPjThreads;
 constexpr int kPjMaxGroup = 1024;
 constexpr int kPjHeads = 4;                                // heads whose scores are asked for together
 
-template <int D, bool kSums>
+template <int D, bool kF8>
 __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr bool kSums = Tile<D, kF8>::kSums;
   constexpr int kWords = D / 4;                            // 16-byte words of a part's row
   constexpr int kParts = kPjThreads / kWords;              // splits read side by side when there are many
   __shared__ float lse2[kPjMaxGroup];                      // log2 units; +inf: nothing to add
@@ -814,6 +825,7 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
     const int w = tid % kWords, part = tid / kWords;
     const float z = lse2[i];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float up = kF8 ? split_scale(p.c.v_scale, h).y : 1.f;        // the parts have the rest of the scale
     if (z != INFINITY) {
 #pragma unroll 4
       for (int j = part; j < q.y; j += kParts) {
@@ -830,7 +842,7 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
         const float4 y = acc_s[o][w];
         acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
       }
-      const __nv_bfloat162 u = __floats2bfloat162_rn(acc.x, acc.y), v = __floats2bfloat162_rn(acc.z, acc.w);
+      const __nv_bfloat162 u = __floats2bfloat162_rn(acc.x * up, acc.y * up), v = __floats2bfloat162_rn(acc.z * up, acc.w * up);
       *reinterpret_cast<uint2*>(p.out + (bg0 + i) * D + 4 * w) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
     }
@@ -906,7 +918,7 @@ static cudaError_t launch_decode_of(const PagedDecodeParams& p, cudaStream_t str
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const int most = p.scores != nullptr ? (p.c.capacity + kPjSlots - 1) / kPjSlots : std::min(p.group, 16);
   const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (148 * 6 + rows - 1) / rows)));
-  return launch_paged(paged_join_kernel<D, Tile<D, kF8>::kSums>, dim3(static_cast<unsigned>(rows), parts), dim3(kPjThreads), 0, 1, stream, p);
+  return launch_paged(paged_join_kernel<D, kF8>, dim3(static_cast<unsigned>(rows), parts), dim3(kPjThreads), 0, 1, stream, p);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int head_dim, bool f8, cudaStream_t stream) {
