@@ -41,7 +41,10 @@ constexpr int kPdMinPage = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // K and V pass through the L2 once: they are the first to leave it, and the scores written meanwhile the last, so that
-// they are still there when the weights are added.
+// they are still there when the weights are added.  They are read as usual then: marked as the first to leave at that
+// last use they cost more (64 x 8 rows of 4,032 slots 190.8 us against 189.5; 96 x 4 e4m3 rows of 8,192 slots 182.3
+// against 180.6, in another process 179.3 against 173.8), and no kernel that ran next was faster for it (matrix
+// products, the dense pass 1, an append, passes over 8 to 96 MB).
 __device__ __forceinline__ uint64_t passing() {
   uint64_t policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
@@ -54,17 +57,6 @@ __device__ __forceinline__ uint64_t staying() {
 }
 __device__ __forceinline__ void store_staying(float* p, float a, float b, uint64_t policy) {
   asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(p), "f"(a), "f"(b), "l"(policy) : "memory");
-}
-// A score's last use: its line is the first to leave the L2 again, so that a call leaves no lines behind that others
-// have to work around (64 x 8 rows of 4,032 slots: 184 us, 186 where they stay; 96 x 4 e4m3 rows of 8,192: 175 and 169,
-// when the next call finds its workspace in the L2).
-__device__ __forceinline__ float4 load_passing(const float* p, uint64_t policy) {
-  float4 v;
-  asm volatile("ld.global.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "l"(p), "l"(policy)
-               : "memory");
-  return v;
 }
 __device__ __forceinline__ void copy16(uint32_t smem, const uint8_t* p, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2;" ::"r"(smem), "l"(p), "l"(policy) : "memory");
@@ -698,7 +690,7 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (i0 + i < G && at0 + u * 4 * kPdThreads < n)
-              s[u][i] = load_passing(p.scores + (bg0 + i0 + i) * p.score_pitch + at0 + u * 4 * kPdThreads, policy);
+              s[u][i] = __ldcg(reinterpret_cast<const float4*>(p.scores + (bg0 + i0 + i) * p.score_pitch + at0 + u * 4 * kPdThreads));
         if (i0 == 0)
 #pragma unroll
           for (int u = 0; u < kU; ++u)
@@ -764,7 +756,6 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
   grid_launch_next();
   const int count = p.c.count[row];
   // A step's pages and scores do not depend on anything: the first step's are on their way from here on.
-  const uint64_t policy = passing();
   const float* scores = p.scores + bg0 * p.score_pitch;
   const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.max_pages;
   int at = blockIdx.y * kPjSlots + 4 * tid;
@@ -774,7 +765,7 @@ __global__ void __launch_bounds__(kPjThreads, 4) paged_join_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < kPjHeads; ++i)
       if (slot < p.c.capacity && g0 + i < p.group)
-        s[i] = load_passing(scores + (g0 + i) * static_cast<int64_t>(p.score_pitch) + slot, policy);
+        s[i] = __ldcg(reinterpret_cast<const float4*>(scores + (g0 + i) * static_cast<int64_t>(p.score_pitch) + slot));
   };
   if (p.scores != nullptr) {
     if (at < p.c.capacity) page = table[at >> p.c.page_shift];
