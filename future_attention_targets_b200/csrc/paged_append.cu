@@ -727,7 +727,8 @@ constexpr int kPsRows = 3 * 148;     // more rows than this are streamed
 // every pass of the select is a barrier of the cluster, and larger clusters
 // wait for room (24 x 8 rows of 16,000 slots: 47, 41, 56 and 121 us with 1, 2,
 // 4 and 8 CTAs per row, since then 38 with 2; 4 x 8 rows: 35, 23 and 33 us with
-// 1, 4 and 8).
+// 1, 4 and 8).  Three CTAs per SM of 512 or 384 threads took 44 to 52 us for the
+// 24 x 8 rows when two took 38.
 cudaError_t launch_paged_append(PagedAppendParams& p, int head_dim, bool f8, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.c.batch) * p.c.n_kv_heads;
   const bool chunk = !p.one_each;

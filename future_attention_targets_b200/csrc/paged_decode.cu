@@ -41,10 +41,10 @@ constexpr int kPdMinPage = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // K and V pass through the L2 once: they are the first to leave it, and the scores written meanwhile the last, so that
-// they are still there when the weights are added.  They are read as usual then: marked as the first to leave at that
-// last use they cost more (64 x 8 rows of 4,032 slots 190.8 us against 189.5; 96 x 4 e4m3 rows of 8,192 slots 182.3
-// against 180.6, in another process 179.3 against 173.8), and no kernel that ran next was faster for it (matrix
-// products, the dense pass 1, an append, passes over 8 to 96 MB).
+// they are still there when the weights are added.  They are read as usual then.  Marked as the first to leave at that
+// last use they cost more (96 x 4 e4m3 rows of 8,192 slots 182.3 us against 180.6 among others, 175 against 169 in a
+// graph; 64 x 8 rows of 4,032 slots 190.8 against 189.5 among others, though 184 against 185.7 in a graph), and no kernel
+// that ran next was faster for it (matrix products, the dense pass 1, an append, passes over 8 to 96 MB).
 __device__ __forceinline__ uint64_t passing() {
   uint64_t policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
@@ -732,6 +732,11 @@ __global__ void __launch_bounds__(kPdThreads, Tile<D, kF8>::ctas(kWide)) paged_d
 // group's heads those with index y modulo gridDim.y.  With lse2 of every head
 // known (a warp each), the parts and scores need one factor:
 //   out = sum over splits of part 2^(max - lse2),  weight[c] += sum over heads of 2^(score - lse2)
+// A cluster of 2 to 16 CTAs per row that joins in distributed shared memory
+// instead was slower for 64 x 8 rows of 4,032 slots (203 us in all, 190 with
+// this kernel): its end has no loads in flight, and large clusters wait for
+// room.  For a few rows, where this kernel is a quarter of the time, it has not
+// been tried.
 // Scores were written moments ago and are mostly still in the L2; what costs
 // is the chain of loads and the few instructions per byte, so a CTA goes
 // through many slots of a row (64 x 8 rows of 4,032 slots: 12.8 us, 18.6 with a

@@ -30,6 +30,9 @@
  * no part (attention), are left unwritten (compaction, append) and are not
  * evicted (append), and *dev_status, if given and still 0, receives
  * KVPOP_ERR_BOUNDS | site << 8 | kernel << 16 for kvpop_check_device_status.
+ * Weights are the caller's data as much as the library's: between calls they
+ * may be replaced, by a scorer's output say, and appends evict by whatever is
+ * there.  An append sets the weight of each new token's slot to 0.
  * A page may not appear twice among the rows that one call writes (the weights
  * count as written by an attention that accumulates); rows that are only read
  * may share pages, such as those of a common prefix.  Positions stay below 2^31.
@@ -81,7 +84,8 @@ typedef struct {
  *   k, v         bf16 [T, n_kv_heads, head_dim], 16-byte aligned (NULL with T = 0)
  *   keep         uint8 [n_kv_heads, T], or NULL to keep every position
  *   score        fp32 [n_kv_heads, T], or NULL for 0 (needs cache->weight_pages otherwise)
- *   cu_seqlens   HOST int32 [batch + 1]; batch = cache->batch at most 512; cu_seqlens[batch] = total_tokens
+ *   cu_seqlens   HOST int32 [batch + 1]; batch = cache->batch at most 512, sequences of at most 131072
+ *                tokens; cu_seqlens[batch] = total_tokens
  * cache->pos_pages, weight_pages and seen are written where they are given. */
 KVPOP_API kvpop_status kvpop_paged_compact_kv(const void* k, const void* v, const uint8_t* keep, const float* score,
                                               const int32_t* cu_seqlens, int32_t total_tokens,
@@ -99,7 +103,8 @@ KVPOP_API kvpop_status kvpop_paged_compact_kv(const void* k, const void* v, cons
  * place among the m_b, its weight 0.  count and seen are advanced.
  *   k_new, v_new   bf16 [T_new, n_kv_heads, head_dim], token_stride elements between tokens
  *                  (a multiple of 8, below 4 GiB; head_dim and heads contiguous), 16-byte aligned
- *   cu_new         HOST int32 [batch + 1], offsets of each sequence's new tokens; NULL = one token each
+ *   cu_new         HOST int32 [batch + 1], offsets of each sequence's new tokens (batch at most 512 then);
+ *                  NULL = one token each
  *   window, sinks  every m_b <= max(window, 1); capacity >= sinks + max(window, 1)
  *   evicted        int32 [T_new, n_kv_heads] or NULL: the position that a token displaced, -1 where it took a
  *                  free slot, -2 where it was not stored
